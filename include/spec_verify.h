@@ -318,6 +318,84 @@ typedef struct {
 int spec_select_gamma(int B, const float* req_stats, const float* comp, spec_gamma_mlp w, int32_t* out_gamma,
                       float* out_expected, void* hip_stream);
 
+/* ---- Training the drafter -------------------------------------------------------------------
+ *
+ * What a drafter learns from the rows that verification reads: the target's largest logits as a
+ * record of each position (spec_row_topk), distillation of draft rows from such records
+ * (spec_topk_distill), and the cross entropy of an LM head's logits that are never in memory
+ * (spec_lm_head_loss).  Each returns its loss per row and, on request, the gradient of
+ * sum_r row_weight[r] loss_r.  The conventions above hold, with these additions: the temperature
+ * is > 0 (SPEC_ERR_INVALID otherwise), the workspace needs no zero-fill and carries nothing from
+ * one call to the next, V <= 2^21 and R <= 2^22 (SPEC_ERR_UNSUPPORTED beyond), every sum is held
+ * in fp32 or fp64 in a fixed order, and the stream belongs to the current device. */
+
+/* spec_row_topk -- the K largest logits of each row, in descending order, equal logits by
+ * ascending index (-0 counts as 0), and the row's log Z.
+ *  K           1..256 (SPEC_ERR_UNSUPPORTED beyond); may exceed V.
+ *  out_index   [R, K] int32; out_logit [R, K] fp32 (the logits, not divided by T).  -inf logits
+ *              are not listed: where a row has fewer than K finite logits the rest of its list is
+ *              index -1, logit -inf.
+ *  out_log_z   [R] fp32 or NULL: ln sum_v exp(l_v / T) over the whole row.
+ * A row with a NaN or +inf logit, or no finite one, gives index -1, logit NaN and log Z NaN.
+ *  workspace   spec_row_topk_workspace_bytes(R, V, K) bytes, 256-byte aligned. */
+int spec_row_topk(int R, int V, int K, spec_dtype dt, const void* logits, int64_t ld, float temperature,
+                  int32_t* out_index, float* out_logit, float* out_log_z, void* workspace, size_t workspace_bytes,
+                  void* hip_stream);
+size_t spec_row_topk_workspace_bytes(int R, int V, int K);
+
+/* spec_topk_distill -- Kullback-Leibler divergence of a student row's q = softmax(s / T) from a
+ * teacher that is known by its largest logits, and its gradient.
+ *  index, teacher_logit  [R, K] int32 and fp32, K in 1..256: tokens x_j and logits t_j, as
+ *              spec_row_topk writes them (the order does not matter).  An entry counts if
+ *              0 <= x_j < V and t_j > -inf; others pad the list.  A token that is listed twice
+ *              counts twice in the sums over the list and is one token of the row.
+ *  teacher_log_z  [R] fp32 or NULL.
+ *    NULL: the list is the teacher, p = softmax(t / T) over it,
+ *          L = sum_j p_j (ln p_j - ln q(x_j)),  dL/ds_v = (q_v - sum_{x_j = v} p_j) / T.
+ *    given (at the same T): p_j = exp(t_j / T - log Z), and rho = max(0, 1 - sum_j p_j) is the
+ *          teacher's mass off the list, set against the student's, q_rho (one outcome "any other
+ *          token"): L = sum_j p_j (ln p_j - ln q(x_j)) + rho (ln rho - ln q_rho); with
+ *          M = sum_j p_j + rho,  dL/ds_v = (M q_v - sum_{x_j = v} p_j) / T for a listed v and
+ *          (M - rho / q_rho) q_v / T for another.  A rho up to 2^-20 counts as 0 (the rounding of
+ *          an fp32 log Z); if rho > 0 and q_rho = 0 the loss is +inf and those logits' gradient 0.
+ *  row_weight  [R] fp32 or NULL (1).
+ *  out_loss    [R] fp32; out_log_z [R] fp32 or NULL: the student's ln sum_v exp(s_v / T).
+ *  d_logits    [R, V] of the logits' type, row stride d_ld, or NULL (no gradient).  May be `logits`
+ *              itself with the same stride: each gradient then replaces its logit.
+ * A row without an entry that counts has loss 0 and gradient 0, one of weight 0 has gradient 0,
+ * whatever its logits are; otherwise a row with a NaN or +inf logit, or no finite one, has a NaN
+ * loss and gradient.
+ *  workspace   spec_topk_distill_workspace_bytes(R, V, K, d_logits != NULL), 256-byte aligned. */
+int spec_topk_distill(int R, int V, int K, spec_dtype dt, const void* logits, int64_t ld, const int32_t* index,
+                      const float* teacher_logit, const float* teacher_log_z, float temperature,
+                      const float* row_weight, float* out_loss, float* out_log_z, void* d_logits, int64_t d_ld,
+                      void* workspace, size_t workspace_bytes, void* hip_stream);
+size_t spec_topk_distill_workspace_bytes(int R, int V, int K, int grad);
+
+/* spec_lm_head_loss -- softmax cross entropy of l = h W^T / T against target tokens, the logits
+ * never in memory, and its gradients: loss_r = ln sum_v exp(l_rv) - l_(r, y_r).
+ *  hidden      [R, D] bf16, row stride h_ld; weight [V, D] bf16, row stride w_ld.  D and every
+ *              stride are multiples of 8 up to 2^21 and every base is 16-byte aligned
+ *              (SPEC_ERR_UNSUPPORTED otherwise).
+ *  targets     [R] int32; a target outside [0, V) leaves its row out: loss 0, no gradient.
+ *  row_weight  [R] fp32 or NULL (1).  A row of weight 0 adds nothing to a gradient, whatever its
+ *              hidden state holds.
+ *  out_loss    [R] fp32; out_log_z [R] fp32 or NULL: ln sum_v exp(l_rv) of every row.
+ *  d_hidden    [R, D] bf16, row stride dh_ld, or NULL; d_weight [V, D] bf16, row stride dw_ld, or
+ *              NULL: gradients of sum_r row_weight[r] loss_r, written whole (not added to).  They
+ *              may not overlap the inputs or each other.  With R = 0 d_weight is zeroed.
+ * The vocabulary is taken in pieces: the workspace, spec_lm_head_loss_workspace_bytes(R, V, D,
+ * d_hidden || d_weight) bytes, 256-byte aligned, holds the logits' gradient (bf16) of one piece,
+ * at most 256 MB or 256 columns.  The logits carry fp32 accumulation error (at most
+ * D 2^-24 sum_d |h_d W_vd|), the gradients bf16 rounding of the logits' gradient and of the result.
+ * A NaN or +inf logit, or no finite one, makes the row's loss NaN, and NaN spreads to the
+ * gradients that the row enters (all of d_weight) unless the row is left out. */
+int spec_lm_head_loss(int R, int V, int D, const void* hidden, int64_t h_ld, const void* weight, int64_t w_ld,
+                      const int32_t* targets, float temperature, const float* row_weight, float* out_loss,
+                      float* out_log_z, void* d_hidden, int64_t dh_ld, void* d_weight, int64_t dw_ld,
+                      void* workspace, size_t workspace_bytes, void* hip_stream);
+size_t spec_lm_head_loss_workspace_bytes(int R, int V, int D, int grad);
+
 /* Benchmark instrumentation, not a verification step: a plain streaming read of `bytes` bytes of
  * device memory at `buf` (16-byte aligned, `bytes` a multiple of 16), the practical HBM read
  * ceiling that a benchmark reports beside the streaming kernel's bandwidth.  `sink` is a device

@@ -16,7 +16,8 @@ __all__ = [
     "SPEC_F32", "SPEC_BF16", "STATUS", "PATHS", "load_library", "library_path", "call_options",
     "spec_verify_batch", "spec_verify_batch_noalloc", "spec_row_stats", "spec_residual_sample", "spec_status_string",
     "spec_verify_workspace_bytes", "spec_row_stats_workspace_bytes",
-    "spec_residual_sample_workspace_bytes",
+    "spec_residual_sample_workspace_bytes", "spec_row_topk", "spec_topk_distill", "spec_lm_head_loss",
+    "spec_row_topk_workspace_bytes", "spec_topk_distill_workspace_bytes", "spec_lm_head_loss_workspace_bytes",
 ]
 
 SPEC_F32 = 0
@@ -122,6 +123,20 @@ def load_library():
     lib.spec_stream_read.argtypes = [vp, i64, vp, vp]
     lib.spec_mfma_rate.restype = i32
     lib.spec_mfma_rate.argtypes = [i32, i32, i32, vp, vp]
+    f32 = ctypes.c_float
+    lib.spec_row_topk.restype = i32
+    lib.spec_row_topk.argtypes = [i32, i32, i32, i32, vp, i64, f32, vp, vp, vp, vp, sz, vp]
+    lib.spec_row_topk_workspace_bytes.restype = sz
+    lib.spec_row_topk_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.spec_topk_distill.restype = i32
+    lib.spec_topk_distill.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, vp, f32, vp, vp, vp, vp, i64, vp, sz, vp]
+    lib.spec_topk_distill_workspace_bytes.restype = sz
+    lib.spec_topk_distill_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.spec_lm_head_loss.restype = i32
+    lib.spec_lm_head_loss.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, f32, vp, vp, vp, vp, i64, vp, i64, vp, sz,
+                                      vp]
+    lib.spec_lm_head_loss_workspace_bytes.restype = sz
+    lib.spec_lm_head_loss_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.spec_status_string.restype = ctypes.c_char_p
     lib.spec_status_string.argtypes = [i32]
     _LIB = lib
@@ -414,4 +429,183 @@ def spec_lm_head_row_stats(hidden, weight, *, temperature=1.0, tokens=None, work
                                        *[_ptr(o.get(k)) for k in HEAD_FIELDS], wsp, wsn, _stream(stream),
                                        _opt_ptr(options))
     _check(rc, "spec_lm_head_row_stats")
+    return o
+
+
+# ---------------------------------------------------------------- training the drafter
+
+_TRAIN_WS = {}   # (device, stream): workspace reused by this section's calls that pass none
+
+
+class _Call:
+    """The device and stream of one training call: the tensors' device, and the given stream or
+    that device's current one, made current inside (so that what the call allocates belongs to
+    the stream its kernels run on)."""
+
+    def __init__(self, t, stream):
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU")
+        self.device = t.device
+        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
+        if self.stream.device != t.device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()   # also makes the stream's device the current one
+        return self
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+    def arg(self, t, name, dtype, shape, optional=False):
+        """A contiguous tensor of this device, type and shape."""
+        if t is None and optional:
+            return None
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def rows(self, t, name, dtype, shape):
+        """A 2-D tensor with unit column stride: its address and row stride."""
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {self.device}")
+        if shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit column stride")
+        if shape[0] > 1 and t.stride(0) < shape[1]:
+            raise ValueError(f"the rows of {name} overlap")
+        return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+
+    def out(self, o, name, dtype, shape):
+        """The caller's output tensor, or a new one."""
+        if o.get(name) is None:
+            o[name] = torch.empty(shape, dtype=dtype, device=self.device)
+        return self.arg(o[name], name, dtype, shape)
+
+    def workspace(self, nbytes, workspace):
+        """The caller's workspace, or one kept per device and stream: calls on one stream are
+        ordered, so they may share it, and one that it has outgrown goes back to that stream's
+        memory.  A call under graph capture that passes none gets a workspace of its own from
+        the graph's memory."""
+        if workspace is not None:
+            n = workspace.numel() * workspace.element_size()
+            if workspace.device != self.device or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on the tensors' device")
+            if n < nbytes:
+                raise ValueError(f"workspace holds {n} bytes, {nbytes} needed")
+            return workspace, n
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device), nbytes
+        key = (self.device, self.stream.cuda_stream)
+        ws = _TRAIN_WS.get(key)
+        if ws is None or ws.numel() < nbytes:
+            _TRAIN_WS.pop(key, None)
+            ws = None
+            ws = _TRAIN_WS[key] = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
+        return ws, ws.numel()
+
+
+def spec_row_topk_workspace_bytes(R, V, K) -> int:
+    return int(load_library().spec_row_topk_workspace_bytes(R, V, K))
+
+
+def spec_topk_distill_workspace_bytes(R, V, K, grad) -> int:
+    return int(load_library().spec_topk_distill_workspace_bytes(R, V, K, int(bool(grad))))
+
+
+def spec_lm_head_loss_workspace_bytes(R, V, D, grad) -> int:
+    return int(load_library().spec_lm_head_loss_workspace_bytes(R, V, D, int(bool(grad))))
+
+
+def spec_row_topk(logits, k, *, temperature=1.0, workspace=None, out=None, stream=None):
+    """The k largest logits of each row with the row's log Z: a teacher's record of its rows (see
+    spec_row_topk in the header).  logits [R, V] bf16 or fp32.  Returns a dict: index [R, k] int32
+    (descending logits, ties by ascending index, -1 past the finite ones), logit [R, k] fp32,
+    log_z [R] fp32 (of logits / temperature); ``out`` may hold any of them."""
+    lib = load_library()
+    if logits.dim() != 2:
+        raise ValueError("logits must be a 2-D tensor")
+    dt = _dtype_code(logits)
+    R, V = logits.shape
+    K = int(k)
+    with _Call(logits, stream) as c:
+        lp, ld = c.rows(logits, "logits", logits.dtype, (R, V))
+        if K <= 0:
+            raise ValueError("k must be positive")
+        o = out if out is not None else {}
+        ptrs = (c.out(o, "index", torch.int32, (R, K)), c.out(o, "logit", torch.float32, (R, K)),
+                c.out(o, "log_z", torch.float32, (R,)))
+        ws, n = c.workspace(lib.spec_row_topk_workspace_bytes(R, V, K), workspace)
+        rc = lib.spec_row_topk(R, V, K, dt, lp, ld, float(temperature), *ptrs, _ptr(ws), n, c.stream.cuda_stream)
+    _check(rc, "spec_row_topk")
+    return o
+
+
+def spec_topk_distill(logits, index, teacher_logit, *, teacher_log_z=None, temperature=1.0, row_weight=None,
+                      grad=False, workspace=None, out=None, stream=None):
+    """Distillation of student rows from a teacher's top logits (see spec_topk_distill in the
+    header).  logits [R, V] bf16 or fp32; index [R, K] int32 and teacher_logit [R, K] fp32 as
+    spec_row_topk returns them; teacher_log_z [R] fp32 adds the teacher's mass off the list as
+    one more outcome, None renormalises the list; row_weight [R] fp32 or None (ones).  Returns a
+    dict: loss [R], log_z [R] (the student's), and with ``grad`` d_logits [R, V], the gradient of
+    sum(row_weight * loss), of the logits' type.  ``out`` may hold any of them; d_logits may be
+    ``logits`` itself."""
+    lib = load_library()
+    if logits.dim() != 2 or index.dim() != 2:
+        raise ValueError("logits and index must be 2-D tensors")
+    dt = _dtype_code(logits)
+    (R, V), K = logits.shape, index.shape[1]
+    with _Call(logits, stream) as c:
+        lp, ld = c.rows(logits, "logits", logits.dtype, (R, V))
+        xp = c.arg(index, "index", torch.int32, (R, K))
+        tp = c.arg(teacher_logit, "teacher_logit", torch.float32, (R, K))
+        zp = c.arg(teacher_log_z, "teacher_log_z", torch.float32, (R,), optional=True)
+        wp = c.arg(row_weight, "row_weight", torch.float32, (R,), optional=True)
+        o = out if out is not None else {}
+        loss, log_z = c.out(o, "loss", torch.float32, (R,)), c.out(o, "log_z", torch.float32, (R,))
+        dp, dld = None, 0
+        if grad:
+            if o.get("d_logits") is None:
+                o["d_logits"] = torch.empty((R, V), dtype=logits.dtype, device=c.device)
+            dp, dld = c.rows(o["d_logits"], "d_logits", logits.dtype, (R, V))
+        ws, n = c.workspace(lib.spec_topk_distill_workspace_bytes(R, V, K, int(bool(grad))), workspace)
+        rc = lib.spec_topk_distill(R, V, K, dt, lp, ld, xp, tp, zp, float(temperature), wp, loss, log_z, dp, dld,
+                                   _ptr(ws), n, c.stream.cuda_stream)
+    _check(rc, "spec_topk_distill")
+    return o
+
+
+def spec_lm_head_loss(hidden, weight, targets, *, temperature=1.0, row_weight=None, grad=False, workspace=None,
+                      out=None, stream=None):
+    """Cross entropy of the LM head's logits hidden @ weight^T / temperature, never materialised,
+    with its gradients (see spec_lm_head_loss in the header).  hidden [R, D] and weight [V, D] are
+    bf16 with unit column stride; targets [R] int32, one outside [0, V) leaves its row out;
+    row_weight [R] fp32 or None (ones).  Returns a dict: loss [R] and log_z [R] fp32, and with
+    ``grad`` (True, or one of "hidden" and "weight") d_hidden [R, D] and / or d_weight [V, D],
+    bf16, of sum(row_weight * loss).  ``out`` may hold any of them."""
+    lib = load_library()
+    if hidden.dim() != 2 or weight.dim() != 2 or hidden.shape[1] != weight.shape[1]:
+        raise ValueError("hidden and weight must be 2-D tensors that share D")
+    if grad not in (True, False, "hidden", "weight"):
+        raise ValueError('grad must be True, False, "hidden" or "weight"')
+    (R, D), V = hidden.shape, weight.shape[0]
+    bf16 = torch.bfloat16
+    with _Call(hidden, stream) as c:
+        hp, hld = c.rows(hidden, "hidden", bf16, (R, D))
+        wtp, wld = c.rows(weight, "weight", bf16, (V, D))
+        yp = c.arg(targets, "targets", torch.int32, (R,))
+        wp = c.arg(row_weight, "row_weight", torch.float32, (R,), optional=True)
+        o = out if out is not None else {}
+        loss, log_z = c.out(o, "loss", torch.float32, (R,)), c.out(o, "log_z", torch.float32, (R,))
+        g = [None, 0, None, 0]
+        for i, (name, rows) in enumerate((("hidden", R), ("weight", V))):
+            if grad is True or grad == name:
+                key = "d_" + name
+                if o.get(key) is None:
+                    o[key] = torch.empty((rows, D), dtype=bf16, device=c.device)
+                g[2 * i:2 * i + 2] = c.rows(o[key], key, bf16, (rows, D))
+        ws, n = c.workspace(lib.spec_lm_head_loss_workspace_bytes(R, V, D, int(bool(grad))), workspace)
+        rc = lib.spec_lm_head_loss(R, V, D, hp, hld, wtp, wld, yp, float(temperature), wp, loss, log_z, *g, _ptr(ws), n,
+                                   c.stream.cuda_stream)
+    _check(rc, "spec_lm_head_loss")
     return o

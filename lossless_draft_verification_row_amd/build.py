@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libspecverify.so"
 SOURCES = ["spec_api.hip", "spec_kernels.hip", "spec_fused.hip", "spec_filter.hip", "spec_head.hip",
-           "spec_noalloc.hip"]
+           "spec_noalloc.hip", "spec_train_api.hip", "spec_topk.hip", "spec_distill.hip", "spec_head_loss.hip"]
 ARCH = os.environ.get("SPEC_OFFLOAD_ARCH", "gfx950")
 
 

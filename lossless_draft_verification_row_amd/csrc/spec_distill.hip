@@ -1,0 +1,254 @@
+// spec_distill.hip -- distillation of logit rows from a teacher's top logits, with its gradient.
+//
+//   q = softmax(s / T) of a student row s; the teacher's list holds tokens x_j with logits t_j.
+//   Without the teacher's log Z the list is the teacher:  p_j = softmax(t / T)_j,  rho = 0.
+//   With it:  p_j = e^(t_j / T - log Z),  rho = max(0, 1 - sum_j p_j)  is the mass off the list.
+//   L = sum_j p_j (ln p_j - ln q_(x_j)) + rho (ln rho - ln q_rho),  q_rho = sum off the list of q
+//   dL/ds_v = (M q_v - sum of p_j with x_j = v) / T on the list, (M - rho / q_rho) q_v / T off it,
+//   M = sum_j p_j + rho.
+// Off the list the gradient is one factor per row times 2^((s_v - m) log2(e) / T), m the largest
+// logit off the list, so that a small q_rho neither underflows nor cancels.  The logits off the
+// list are summed without those on it (never as a difference of sums).
+//
+//   k_td_stats  one workgroup per 8192 logits of a row: maximum and sum of exponentials off the list
+//   k_td_loss   one workgroup per row: those and the list -> loss, log Z, the gradient's factors
+//   k_td_grad   one workgroup per 8192 logits of a row: the gradient
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "spec_device.h"
+#include "spec_train.h"
+
+namespace specv {
+
+constexpr int kTdPer = kTrSeg / kThreads;   // 32 logits per thread
+constexpr double kTdTailMin = 0x1p-20;      // mass off the list that counts: below it is the
+                                            // rounding of an fp32 log Z
+
+template <int DT>
+struct TdEl {
+  static constexpr int n = DT == kDtBF16 ? 8 : 4;   // logits of a 16-byte vector
+};
+template <int DT>
+__device__ __forceinline__ int td_index(int j) {
+  constexpr int kEl = TdEl<DT>::n;
+  return kEl * ((int)threadIdx.x + kThreads * (j / kEl)) + j % kEl;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void td_load(const void* row, int V, int base, float (&v)[kTdPer]) {
+  constexpr int kEl = TdEl<DT>::n;
+#pragma unroll
+  for (int q = 0; q < kTdPer / kEl; ++q) {
+    const int e0 = base + td_index<DT>(q * kEl);
+    if (VEC && e0 + kEl <= V) {
+      const uint4 x = ld_nt16((const char*)row + (int64_t)e0 * (16 / kEl));
+      if constexpr (DT == kDtBF16) {
+        v[8 * q + 0] = bf16_lo(x.x); v[8 * q + 1] = bf16_hi(x.x); v[8 * q + 2] = bf16_lo(x.y); v[8 * q + 3] = bf16_hi(x.y);
+        v[8 * q + 4] = bf16_lo(x.z); v[8 * q + 5] = bf16_hi(x.z); v[8 * q + 6] = bf16_lo(x.w); v[8 * q + 7] = bf16_hi(x.w);
+      } else {
+        v[4 * q + 0] = __uint_as_float(x.x); v[4 * q + 1] = __uint_as_float(x.y);
+        v[4 * q + 2] = __uint_as_float(x.z); v[4 * q + 3] = __uint_as_float(x.w);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kEl; ++e) v[kEl * q + e] = e0 + e < V ? logit_at<DT>(row, e0 + e) : -INFINITY;
+    }
+  }
+}
+__device__ __forceinline__ uint32_t td_pack(float a, float b) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+template <int DT>
+__device__ __forceinline__ void td_put(void* row, int i, float x) {
+  if constexpr (DT == kDtBF16) ((__bf16*)row)[i] = (__bf16)x;
+  else ((float*)row)[i] = x;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void td_store(void* row, int V, int base, const float (&v)[kTdPer]) {
+  constexpr int kEl = TdEl<DT>::n;
+#pragma unroll
+  for (int q = 0; q < kTdPer / kEl; ++q) {
+    const int e0 = base + td_index<DT>(q * kEl);
+    if (VEC && e0 + kEl <= V) {
+      uint4 x;
+      if constexpr (DT == kDtBF16)
+        x = make_uint4(td_pack(v[8 * q], v[8 * q + 1]), td_pack(v[8 * q + 2], v[8 * q + 3]),
+                       td_pack(v[8 * q + 4], v[8 * q + 5]), td_pack(v[8 * q + 6], v[8 * q + 7]));
+      else
+        x = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                       __float_as_uint(v[4 * q + 3]));
+      *(uint4*)((char*)row + (int64_t)e0 * (16 / kEl)) = x;
+    } else {
+#pragma unroll
+      for (int e = 0; e < kEl; ++e)
+        if (e0 + e < V) td_put<DT>(row, e0 + e, v[kEl * q + e]);
+    }
+  }
+}
+
+// Entry j of row r's list: its token, or -1 for one that does not count (a token outside the
+// vocabulary, a logit of -inf).
+__device__ __forceinline__ int td_token(const DistillArgs& a, int64_t r, int j, float& t) {
+  if (j >= a.K) return -1;
+  const int x = a.index[r * a.K + j];
+  t = a.teacher[r * a.K + j];
+  return x >= 0 && x < a.V && t != -INFINITY ? x : -1;
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_td_stats(DistillArgs a) {
+  __shared__ uint32_t listed[kTrSeg / 32];   // a bit per logit of the segment
+  __shared__ float red[2 * kWaves];
+  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * kTrSeg, t = threadIdx.x;
+  float v[kTdPer];
+  td_load<DT, VEC>(row_ptr<DT>(a.logits, a.ld, r), a.V, base, v);
+  listed[t] = 0;
+  __syncthreads();
+  float tl;
+  const int x = td_token(a, r, t, tl) - base;
+  if (x >= 0 && x < kTrSeg) atomicOr(&listed[x >> 5], 1u << (x & 31));
+  __syncthreads();
+  constexpr int kEl = TdEl<DT>::n;
+  float m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kTdPer / kEl; ++q) {
+    const int i = td_index<DT>(q * kEl);
+    const uint32_t b = listed[i >> 5] >> (i & 31);
+#pragma unroll
+    for (int e = 0; e < kEl; ++e) {
+      if (b & (1u << e)) v[kEl * q + e] = -INFINITY;
+      m = fmaxf(m, v[kEl * q + e]);
+    }
+  }
+  m = block_max(m, red);
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < kTdPer; ++j) {
+    // nothing but -inf (or a NaN, which fmaxf passes over and the sum then shows)
+    const float d = m > -INFINITY ? v[j] - m : v[j];
+    s += __builtin_amdgcn_exp2f(d * a.c);
+  }
+  s = wave_sum(s);
+  if ((t & 63) == 0) red[t >> 6] = s;
+  __syncthreads();
+  if (t == 0) a.ms[(int64_t)r * a.n_seg + seg] = MaxSum{m, (red[0] + red[1]) + (red[2] + red[3])};
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_td_loss(DistillArgs a) {
+  __shared__ int lx[kTrMaxK];
+  __shared__ double lp[kTrMaxK];
+  __shared__ float red[2 * kWaves];
+  __shared__ int redi[2 * kWaves];
+  __shared__ double redd[kWaves];
+  const int r = blockIdx.x, t = threadIdx.x;
+  const MaxSum* ms = a.ms + (int64_t)r * a.n_seg;
+  float tl = -INFINITY;
+  const int x = td_token(a, r, t, tl);
+  lx[t] = x;
+  __syncthreads();
+  bool first = x >= 0;   // the same token twice is one place of the row
+  for (int j = 0; j < t && first; ++j) first = lx[j] != x;
+  const float l = x >= 0 ? logit_at<DT>(row_ptr<DT>(a.logits, a.ld, r), x) : -INFINITY;
+  const int some = block_or(x >= 0 ? 1 : 0, redi);
+
+  // the row: off the list relative to m_out, all of it relative to m
+  float m_out = -INFINITY;
+  for (int i = t; i < a.n_seg; i += kThreads) m_out = fmaxf(m_out, ms[i].m);
+  m_out = block_max(m_out, red);
+  double z_out = 0.0;
+  for (int i = t; i < a.n_seg; i += kThreads)
+    z_out += ms[i].m > -INFINITY ? (double)ms[i].s * (double)__builtin_amdgcn_exp2f((ms[i].m - m_out) * a.c)
+                                 : (double)ms[i].s;
+  z_out = block_sum_d(z_out, redd);
+  const float m = fmaxf(m_out, block_max(l, red));
+  const double e_l = x >= 0 ? exp2_split(((double)l - (double)m) * (double)a.c) : 0.0;
+  const double f_out = m_out > -INFINITY ? exp2_split(((double)m_out - (double)m) * (double)a.c) : 0.0;
+  double z = block_sum_d(first ? e_l : 0.0, redd) + (m_out > -INFINITY ? z_out * f_out : z_out);
+  if (!(m > -INFINITY)) z = __longlong_as_double(0x7ff8000000000000ll);   // no finite logit
+  const double lz = (double)m * a.inv_t + log(z);
+
+  // the teacher
+  double ln_p = -INFINITY, p = 0.0, rho = 0.0;
+  const float tm = block_max(x >= 0 ? tl : -INFINITY, red);
+  if (a.teacher_log_z) {
+    if (x >= 0) ln_p = (double)tl * a.inv_t - (double)a.teacher_log_z[r];
+  } else {
+    const double zt = block_sum_d(x >= 0 ? exp(((double)tl - (double)tm) * a.inv_t) : 0.0, redd);
+    if (x >= 0) ln_p = ((double)tl - (double)tm) * a.inv_t - log(zt);
+  }
+  if (x >= 0) p = exp(ln_p);
+  lp[t] = p;
+  const double sum_p = block_sum_d(p, redd);
+  if (a.teacher_log_z) {
+    rho = 1.0 - sum_p;
+    if (rho <= kTdTailMin) rho = 0.0;
+  }
+  const double term = p > 0.0 ? p * (ln_p - ((double)l * a.inv_t - lz)) : p;   // p is 0, or NaN
+  double loss = block_sum_d(term, redd);
+  if (rho > 0.0) loss += rho * (log(rho) - (z_out > 0.0 ? (double)m_out * a.inv_t + log(z_out) - lz : -INFINITY));
+  if (z != z) loss = z;
+  if (t == 0) {
+    if (a.loss) a.loss[r] = some ? (float)loss : 0.f;
+    if (a.log_z) a.log_z[r] = (float)lz;
+  }
+  if (!a.d_logits) return;
+  const double scale = (a.row_weight ? (double)a.row_weight[r] : 1.0) * a.inv_t, mass = sum_p + rho;
+  if (t == 0) {
+    DistillRow o;
+    o.m = m_out > -INFINITY ? m_out : 0.f;   // nothing off the list: its -inf logits give 0, not NaN
+    o.f = (float)(scale * (mass * f_out / z - (rho > 0.0 && z_out > 0.0 ? rho / z_out : 0.0)));
+    o.zero = !some || scale == 0.0 ? 1 : 0;
+    o.pad = 0;
+    a.rows[r] = o;
+  }
+  if (x >= 0) {
+    double ps = 0.0;
+    for (int j = 0; j < a.K; ++j) ps += lx[j] == x ? lp[j] : 0.0;
+    a.d_list[(int64_t)r * a.K + t] = (float)(scale * (mass * e_l / z - ps));
+  }
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_td_grad(DistillArgs a) {
+  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * kTrSeg;
+  void* out = const_cast<void*>(row_ptr<DT>(a.d_logits, a.d_ld, r));
+  const DistillRow row = a.rows[r];
+  float v[kTdPer];
+  if (row.zero) {
+#pragma unroll
+    for (int j = 0; j < kTdPer; ++j) v[j] = 0.f;
+    td_store<DT, VEC>(out, a.V, base, v);
+    return;
+  }
+  td_load<DT, VEC>(row_ptr<DT>(a.logits, a.ld, r), a.V, base, v);
+#pragma unroll
+  for (int j = 0; j < kTdPer; ++j) v[j] = __builtin_amdgcn_exp2f((v[j] - row.m) * a.c) * row.f;
+  td_store<DT, VEC>(out, a.V, base, v);
+  wait_vmem();       // the list's tokens are written over what this stored
+  __syncthreads();
+  float tl;
+  const int x = td_token(a, r, threadIdx.x, tl);
+  if (x >= base && x < base + kTrSeg) td_put<DT>(out, x, a.d_list[(int64_t)r * a.K + threadIdx.x]);
+}
+
+namespace {
+template <int DT, bool VEC>
+void topk_distill(const DistillArgs& a, hipStream_t st) {
+  const dim3 segs((unsigned)(a.R * a.n_seg)), block(kThreads);
+  hipLaunchKernelGGL((k_td_stats<DT, VEC>), segs, block, 0, st, a);
+  hipLaunchKernelGGL((k_td_loss<DT>), dim3((unsigned)a.R), block, 0, st, a);
+  if (a.d_logits) hipLaunchKernelGGL((k_td_grad<DT, VEC>), segs, block, 0, st, a);
+}
+}  // namespace
+
+hipError_t launch_topk_distill(const DistillArgs& a, int dt, int vec, hipStream_t st) {
+  if (dt == kDtBF16) vec ? topk_distill<kDtBF16, true>(a, st) : topk_distill<kDtBF16, false>(a, st);
+  else vec ? topk_distill<kDtF32, true>(a, st) : topk_distill<kDtF32, false>(a, st);
+  return hipGetLastError();
+}
+
+}  // namespace specv

@@ -1,0 +1,496 @@
+// spec_head_loss.hip -- softmax cross entropy of the LM head's logits, with its gradient, without
+// the logits in memory.
+//
+//   l_rv = sum_d h_rd W_vd,   loss_r = ln sum_v e^(l_rv / T) - l_(r, y_r) / T
+//   G_rv = w_r (softmax(l_r / T)_v - [v = y_r]) / T,   dh = G W,   dW = G^T h
+//
+// Forward: every 256-column tile of the logits leaves a maximum and a sum of exponentials per
+// row, which one small kernel folds.  Gradient: the vocabulary is taken in pieces; a piece's
+// logits are formed again, turned into G (bf16) and used at once in the two products, so that
+// the workspace holds G of one piece (at most 256 MB), never that of the whole vocabulary when
+// that is larger.  Work: 2RVD for the loss and 6RVD more for the gradient.
+//
+//   k_hl_prep     the target's logit, the row's scale, the hidden rows with those left out zeroed
+//   k_hl_stats    logit tiles -> (maximum, sum) per row and tile
+//   k_hl_rows     those -> log Z and the loss
+//   k_hl_grad     logit tiles -> G of one piece
+//   k_hl_dhidden  G W over a piece, fp32 parts kept per split of the piece
+//   k_hl_dweight  G^T h of a piece
+//   k_hl_reduce   the parts -> d_hidden
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "spec_device.h"
+#include "spec_train.h"
+
+namespace specv {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_void_t;
+typedef __attribute__((address_space(3))) s16x4* lds_s4_t;
+
+// One matrix operand of a product: 256 (or BN) rows of the tile against kHlDepth k per stage.
+//   k contiguous (KM false): element (row, k) at p[row ld + k]; `p` is the tile's first row.
+//   k major      (KM true):  element (row, k) at p[k ld + row]; `p` is the tile's first column.
+// `bytes` is what lies between p and the end of the matrix's last row: loads past it return
+// zeros.  A k-contiguous operand's k past `k_end` also reads as zero.
+struct HlOperand {
+  const uint16_t* p;
+  int64_t ld;
+  int64_t bytes;
+};
+
+constexpr int kGran = kHlDepth / 8;    // 16-byte granules of a k-contiguous row per stage
+constexpr int kFarOffset = 0x7ffffff0;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t stage_rsrc(const HlOperand& o, int64_t skip) {
+  const int64_t left = o.bytes - skip;
+  const int n = left < 0 ? 0 : left > (int64_t)kFarOffset ? kFarOffset : (int)left;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)o.p + skip), (short)0, n, 0x00020000);
+}
+
+// Within a k-contiguous row the granules are permuted by an XOR of the row's low bits, within a
+// k-major row (one k, all rows of the tile) by 4 (k % 4), so that a fragment read's phases fall
+// into distinct banks.
+__device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// Tile product core: acc[i][j] += A rows (32 (TI wr + i) ..) x B rows (32 (TJ wc + j) ..), A and B
+// 256 and BN rows wide, four waves as WRN x (4 / WRN).  The 32x32x16 MFMA's C has the A row in
+// the element (8 (e / 4) + 4 (lane / 32) + e % 4) and the B row in the lane (lane % 32).
+template <int TI, int TJ, int WRN, bool KMA, bool KMB>
+struct HlCore {
+  static constexpr int WCN = kWaves / WRN;
+  static constexpr int BN = 32 * TJ * WCN;
+  static constexpr int NA = kHlTile * kGran / kThreads;   // granules per thread and stage
+  static constexpr int NB = BN * kGran / kThreads;
+  static_assert(32 * TI * WRN == kHlTile, "A is 256 rows wide");
+  static_assert(!KMB || BN == kHlTile, "a k-major B is 256 rows wide");
+  struct Lds {
+    uint4 a[2][kHlTile * kGran];
+    uint4 b[2][BN * kGran];
+  };
+
+  // byte offset within a stage of the granule that this thread's load n fills
+  template <bool KM, int N>
+  static __device__ __forceinline__ int load_offset(int n, int wave, int lane, int64_t ld) {
+    const int p = 64 * (N * wave + n) + lane;
+    if constexpr (KM) {
+      const int k = p >> 5, g = (p & 31) ^ (4 * (k & 3));
+      return (int)(k * ld * 2) + 16 * g;
+    } else {
+      const int r = p >> 3, g = (p & 7) ^ swz_row(r);
+      return (int)(r * ld * 2) + 16 * g;
+    }
+  }
+  template <bool KM, int N>
+  static __device__ __forceinline__ void load(uint4* lds, __amdgpu_buffer_rsrc_t rs, const int (&v)[N], int wave,
+                                              int lane, int k_left) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      int off = v[n];
+      if constexpr (!KM) {   // a granule past the row's end reads as zero
+        const int p = 64 * (N * wave + n) + lane;
+        if (8 * ((p & 7) ^ swz_row(p >> 3)) >= k_left) off = kFarOffset;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t)&lds[64 * (N * wave + n)], 16, off, 0, 0, 0);
+    }
+  }
+  // fragment of 32 rows from `row0`, k 16 h .. 16 h + 15 of the stage
+  template <bool KM>
+  static __device__ __forceinline__ bf16x8 frag(const uint4* lds, int row0, int h, int lane) {
+    if constexpr (KM) {
+      // each 16 lanes read a 4 (k) x 16 (rows) block transposed: lane q of them addresses k q / 4,
+      // rows 4 (q % 4) .., and receives row q's four k
+      const int q = lane & 15, g = row0 / 8 + 2 * ((lane >> 4) & 1) + ((q & 3) >> 1);
+      const int k = 16 * h + 8 * (lane >> 5) + (q >> 2);
+      const char* p = (const char*)lds + 16 * (k * 32 + (g ^ (4 * (q >> 2)))) + 8 * (q & 1);
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)(p + 4 * 512));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int r = row0 + (lane & 31);
+      return __builtin_bit_cast(bf16x8, lds[r * kGran + ((2 * h + (lane >> 5)) ^ swz_row(r))]);
+    }
+  }
+
+  // n_k stages; k_len (of a k-contiguous operand) beyond which k reads as zero
+  static __device__ __forceinline__ void run(Lds& L, const HlOperand& A, const HlOperand& B, int n_k, int k_len,
+                                             f32x16 (&acc)[TI][TJ]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = wave / WCN, wc = wave % WCN;
+    const int64_t sa = (KMA ? kHlDepth * A.ld : kHlDepth) * 2, sb = (KMB ? kHlDepth * B.ld : kHlDepth) * 2;
+    int va[NA], vb[NB];
+#pragma unroll
+    for (int n = 0; n < NA; ++n) va[n] = load_offset<KMA, NA>(n, wave, lane, A.ld);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) vb[n] = load_offset<KMB, NB>(n, wave, lane, B.ld);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    load<KMA, NA>(L.a[0], stage_rsrc(A, 0), va, wave, lane, k_len);
+    load<KMB, NB>(L.b[0], stage_rsrc(B, 0), vb, wave, lane, k_len);
+    for (int s = 0; s < n_k; ++s) {
+      // this wave's loads of stage s have landed, and after the barrier everyone's; every wave is
+      // also done with the other buffer, which the next stage's loads now fill
+      wait_vmem();
+      __syncthreads();
+      if (s + 1 < n_k) {
+        load<KMA, NA>(L.a[(s + 1) & 1], stage_rsrc(A, (s + 1) * sa), va, wave, lane, k_len - kHlDepth * (s + 1));
+        load<KMB, NB>(L.b[(s + 1) & 1], stage_rsrc(B, (s + 1) * sb), vb, wave, lane, k_len - kHlDepth * (s + 1));
+      }
+      const uint4 *la = L.a[s & 1], *lb = L.b[s & 1];
+#pragma unroll
+      for (int h = 0; h < kHlDepth / 16; ++h) {
+        bf16x8 fa[TI], fb[TJ];
+#pragma unroll
+        for (int i = 0; i < TI; ++i) fa[i] = frag<KMA>(la, 32 * (TI * wr + i), h, lane);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) fb[j] = frag<KMB>(lb, 32 * (TJ * wc + j), h, lane);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int j = 0; j < TJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      }
+    }
+    wait_vmem();       // (without a stage: the first one's loads)
+    __syncthreads();   // every wave is done with the stage buffers
+  }
+};
+
+// What lies between element (row, col) of a [rows, cols] matrix and the end of its last row.
+__device__ __forceinline__ int64_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t row, int64_t col) {
+  return ((rows - 1 - row) * ld + cols - col) * 2;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// One wave per row (rows past R are set up as left out): the target's logit in fp32, the scale
+// of the row's gradient, and the hidden row with a row that is left out zeroed, so that what it
+// holds (padding may be NaN) never meets a product.
+__global__ __launch_bounds__(kThreads) void k_hl_prep(HlArgs a, int grad) {
+  const int lane = threadIdx.x & 63, r = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  if (r >= a.plan.Rp) return;
+  int y = r < a.R ? a.targets[r] : -1;
+  if (y >= a.V || y < 0) y = -1;
+  const float w = y < 0 ? 0.f : a.row_weight ? a.row_weight[r] : 1.f;
+  const uint4* h = (const uint4*)(a.hidden + (int64_t)(r < a.R ? r : 0) * a.h_ld);
+  const uint4* wy = (const uint4*)(a.weight + (int64_t)(y < 0 ? 0 : y) * a.w_ld);
+  uint4* hz = (uint4*)(a.hz + (int64_t)r * a.D);
+  float s = 0.f;
+  for (int k = lane; k < a.D / 8; k += 64) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (y >= 0) {
+      x = h[k];
+      const uint4 v = wy[k];
+      s = fmaf(bf16_lo(x.x), bf16_lo(v.x), s); s = fmaf(bf16_hi(x.x), bf16_hi(v.x), s);
+      s = fmaf(bf16_lo(x.y), bf16_lo(v.y), s); s = fmaf(bf16_hi(x.y), bf16_hi(v.y), s);
+      s = fmaf(bf16_lo(x.z), bf16_lo(v.z), s); s = fmaf(bf16_hi(x.z), bf16_hi(v.z), s);
+      s = fmaf(bf16_lo(x.w), bf16_lo(v.w), s); s = fmaf(bf16_hi(x.w), bf16_hi(v.w), s);
+    }
+    if (grad) hz[k] = w == 0.f ? make_uint4(0u, 0u, 0u, 0u) : x;
+  }
+  s = wave_sum(s);
+  if (lane == 0) {
+    a.ly[r] = s;
+    HlRow o;
+    o.lz2 = 0.f;
+    o.scale = (float)((double)w * a.inv_t);
+    o.y = y;
+    o.pad = 0;
+    a.rows[r] = o;
+  }
+}
+
+template <int TI, int TJ, int WRN>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_stats(HlArgs a, int n_rt) {
+  using Core = HlCore<TI, TJ, WRN, false, false>;
+  __shared__ typename Core::Lds L;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / Core::WCN, wc = wave % Core::WCN;
+  const int jx = blockIdx.x >> 3, rt = jx % n_rt, ct = (jx / n_rt) * 8 + (blockIdx.x & 7);
+  if (ct >= a.plan.n_ct) return;
+  const int v0 = ct * kHlTile, r0 = rt * Core::BN;
+  f32x16 acc[TI][TJ];
+  const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
+  const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
+  Core::run(L, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
+
+  // A lane holds 16 TI columns of TJ rows; lane ^ 32 holds the rows' other columns of this wave,
+  // the other WRN - 1 waves those of the tile.  -inf keeps its weight 0; a NaN or +inf logit makes
+  // the sum NaN (inf - inf), also where it is all that a lane holds.
+  float2* part = (float2*)&L;   // [WRN][BN]
+  const int vl = v0 + 32 * TI * wr + 4 * (lane >> 5);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    if (v0 + kHlTile > a.V) {   // the vocabulary's last tile
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[i][j][e] = vl + 32 * i + 8 * (e >> 2) + (e & 3) < a.V ? acc[i][j][e] : -INFINITY;
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
+    m = fmaxf(m, __shfl_xor(m, 32));
+    float s = 0.f;
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * a.c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (acc[i][j][e] != acc[i][j][e]) s = acc[i][j][e];
+    }
+    s += __shfl_xor(s, 32);
+    if (lane < 32) part[wr * Core::BN + 32 * (TJ * wc + j) + lane] = make_float2(m, s);
+  }
+  __syncthreads();
+  for (int t = threadIdx.x; t < Core::BN; t += kThreads) {
+    const int r = r0 + t;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int k = 0; k < WRN; ++k) m = fmaxf(m, part[k * Core::BN + t].x);
+#pragma unroll
+    for (int k = 0; k < WRN; ++k) {
+      const float2 p = part[k * Core::BN + t];
+      if (p.x > -INFINITY) s += p.y * __builtin_amdgcn_exp2f((p.x - m) * a.c);
+      else s += p.y;   // 0, or a NaN
+    }
+    if (r < a.plan.Rp) a.rec[(int64_t)ct * a.plan.Rp + r] = make_float2(m, s);
+  }
+}
+
+// Sixteen rows per workgroup, sixteen threads to a row: the tiles' records in fp64.
+__global__ __launch_bounds__(kThreads) void k_hl_rows(HlArgs a) {
+  __shared__ float sm[16][17];
+  __shared__ double ss[16][17];
+  const int q = threadIdx.x >> 4, rl = threadIdx.x & 15;
+  const int r = blockIdx.x * 16 + rl;
+  float m = -INFINITY;
+  if (r < a.R)
+    for (int k = q; k < a.plan.n_ct; k += 16) m = fmaxf(m, a.rec[(int64_t)k * a.plan.Rp + r].x);
+  sm[rl][q] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) m = fmaxf(m, sm[rl][k]);
+  double s = 0.0;
+  if (r < a.R)
+    for (int k = q; k < a.plan.n_ct; k += 16) {
+      const float2 p = a.rec[(int64_t)k * a.plan.Rp + r];
+      s += p.x > -INFINITY ? (double)p.y * (double)__builtin_amdgcn_exp2f((p.x - m) * a.c) : (double)p.y;
+    }
+  ss[rl][q] = s;
+  __syncthreads();
+  if (q != 0 || r >= a.R) return;
+  double z = 0.0;
+  for (int k = 0; k < 16; ++k) z += ss[rl][k];
+  const double nan = __longlong_as_double(0x7ff8000000000000ll);
+  const double l2 = z > 0.0 ? log2_split(z) : nan;
+  const double lz = (double)m * a.inv_t + l2 * 0.6931471805599453;
+  if (a.log_z) a.log_z[r] = (float)lz;
+  if (a.loss) a.loss[r] = a.rows[r].y < 0 ? 0.f : (float)(lz - (double)a.ly[r] * a.inv_t);
+  a.rows[r].lz2 = (float)((double)m * (double)a.c + l2);
+}
+
+// G of one piece: columns v0 .. v0 + n_v - 1 (n_v a multiple of 64 but for the vocabulary's end;
+// the columns up to the next multiple of 64 are written as zeros, as are rows R .. Rp - 1).
+template <int TI, int TJ, int WRN>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_grad(HlArgs a, int pv0,
+                                                                                                int n_v, int n_rt) {
+  using Core = HlCore<TI, TJ, WRN, false, false>;
+  __shared__ typename Core::Lds L;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / Core::WCN, wc = wave % Core::WCN;
+  const int jx = blockIdx.x >> 3, rt = jx % n_rt, ct = (jx / n_rt) * 8 + (blockIdx.x & 7);
+  if (ct * kHlTile >= n_v) return;
+  const int v0 = pv0 + ct * kHlTile, r0 = rt * Core::BN;
+  f32x16 acc[TI][TJ];
+  const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
+  const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
+  Core::run(L, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
+  const int n_vp = (n_v + kHlDepth - 1) / kHlDepth * kHlDepth;
+  const int vt = 32 * TI * wr + 4 * (lane >> 5);      // the lane's first column within the tile
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    const int r = r0 + 32 * (TJ * wc + j) + (lane & 31);
+    if (r >= a.plan.Rp) continue;
+    const HlRow row = a.rows[r];
+    uint16_t* g = a.g + (int64_t)r * a.plan.piece + ct * kHlTile;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int v = vt + 32 * i + 8 * q;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + e], a.c, -row.lz2));
+          x[e] = (v0 + v + e == row.y ? p - 1.f : p) * row.scale;
+          if (row.scale == 0.f || v0 + v + e >= a.V) x[e] = 0.f;
+        }
+        // G is rounded to bf16 (half a step, 2^-9 of each entry): both products take bf16
+        // operands, and the errors of a row's entries are independent
+        if (ct * kHlTile + v < n_vp) *(uint2*)(g + v) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      }
+  }
+}
+
+// dh[r][d] over columns of the piece: k = v, A = W (k major, rows d), B = G (k contiguous).
+template <int TI, int TJ, int WRN>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_dhidden(
+    HlArgs a, int pv0, int n_v, int n_rt, int n_dt, int add) {
+  using Core = HlCore<TI, TJ, WRN, true, false>;
+  __shared__ typename Core::Lds L;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / Core::WCN, wc = wave % Core::WCN;
+  const int dt = blockIdx.x % n_dt, rt = blockIdx.x / n_dt % n_rt, sp = blockIdx.x / n_dt / n_rt;
+  const int d0 = dt * kHlTile, r0 = rt * Core::BN;
+  // this split's stages of the piece
+  const int n_st = (n_v + kHlDepth - 1) / kHlDepth;
+  const int s0 = (int)((int64_t)n_st * sp / a.plan.n_split), s1 = (int)((int64_t)n_st * (sp + 1) / a.plan.n_split);
+  const int k0 = s0 * kHlDepth;
+  f32x16 acc[TI][TJ];
+  const HlOperand A = {a.weight + (int64_t)(pv0 + k0) * a.w_ld + d0, a.w_ld,
+                       extent(a.V, a.D, a.w_ld, pv0 + k0, d0)};
+  const HlOperand B = {a.g + (int64_t)r0 * a.plan.piece + k0, a.plan.piece,
+                       extent(a.plan.Rp, a.plan.piece, a.plan.piece, r0, k0)};
+  Core::run(L, A, B, s1 - s0, (s1 - s0) * kHlDepth, acc);
+  float* part = a.part + (int64_t)sp * a.plan.Rp * a.D;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    const int r = r0 + 32 * (TJ * wc + j) + (lane & 31);
+    if (r >= a.plan.Rp) continue;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int d = d0 + 32 * (TI * wr + i) + 8 * q + 4 * (lane >> 5);
+        if (d < a.D) {
+          float4* p = (float4*)(part + (int64_t)r * a.D + d);
+          float4 x = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+          if (add) {
+            const float4 o = *p;
+            x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
+          }
+          *p = x;
+        }
+      }
+  }
+}
+
+// dW[v][d] of the piece: k = r, A = h (k major, rows d), B = G (k major, rows v).
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_hl_dweight(HlArgs a, int pv0,
+                                                                                                   int n_v, int n_dt) {
+  constexpr int TI = 4, TJ = 4, WRN = 2;
+  using Core = HlCore<TI, TJ, WRN, true, true>;
+  __shared__ typename Core::Lds L;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / Core::WCN, wc = wave % Core::WCN;
+  const int dt = blockIdx.x % n_dt, ct = blockIdx.x / n_dt;
+  const int d0 = dt * kHlTile, vt0 = ct * kHlTile;
+  f32x16 acc[TI][TJ];
+  const HlOperand A = {a.hz + d0, a.D, extent(a.plan.Rp, a.D, a.D, 0, d0)};
+  const HlOperand B = {a.g + vt0, a.plan.piece, extent(a.plan.Rp, a.plan.piece, a.plan.piece, 0, vt0)};
+  Core::run(L, A, B, a.plan.Rp / kHlDepth, a.plan.Rp, acc);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    const int vl = vt0 + 32 * (TJ * wc + j) + (lane & 31);
+    if (vl >= n_v) continue;
+    uint16_t* o = a.d_weight + (int64_t)(pv0 + vl) * a.dw_ld;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int d = d0 + 32 * (TI * wr + i) + 8 * q + 4 * (lane >> 5);
+        if (d < a.D)
+          *(uint2*)(o + d) = make_uint2(pack_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                                        pack_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
+      }
+  }
+}
+
+// d_hidden = the splits' parts, added in order, rounded once.
+__global__ __launch_bounds__(kThreads) void k_hl_reduce(HlArgs a) {
+  const int64_t n4 = (int64_t)a.R * (a.D / 4), i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n4) return;
+  const int64_t r = i / (a.D / 4), d = i % (a.D / 4) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < a.plan.n_split; ++k) {
+    const float4 p = *(const float4*)(a.part + ((int64_t)k * a.plan.Rp + r) * a.D + d);
+    s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
+  }
+  *(uint2*)(a.d_hidden + r * a.dh_ld + d) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+// The head's gradient of an empty batch.
+__global__ __launch_bounds__(kThreads) void k_hl_zero(uint16_t* p, int64_t ld, int V, int D) {
+  const int64_t n8 = D / 8, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i < V * n8) *(uint4*)(p + i / n8 * ld + i % n8 * 8) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+hipError_t launch_head_zero(uint16_t* d_weight, int64_t ld, int V, int D, hipStream_t st) {
+  const int64_t n = (int64_t)V * (D / 8);
+  hipLaunchKernelGGL(k_hl_zero, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, d_weight, ld, V, D);
+  return hipGetLastError();
+}
+
+namespace {
+
+template <int TI, int TJ, int WRN>
+hipError_t head_loss(const HlArgs& a, hipStream_t st) {
+  const HlPlan& p = a.plan;
+  const bool grad = a.d_hidden || a.d_weight;
+  const int n_rt = (a.R + p.bn - 1) / p.bn, n_dt = (a.D + kHlTile - 1) / kHlTile;
+  hipLaunchKernelGGL(k_hl_prep, dim3((unsigned)((p.Rp + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a, grad ? 1 : 0);
+  hipLaunchKernelGGL((k_hl_stats<TI, TJ, WRN>), dim3((unsigned)((p.n_ct + 7) / 8 * 8 * n_rt)), dim3(kThreads), 0, st, a,
+                     n_rt);
+  hipLaunchKernelGGL(k_hl_rows, dim3((unsigned)((a.R + 15) / 16)), dim3(kThreads), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !grad) return e;
+  for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
+    const int n_v = (int)(a.V - v0 < p.piece ? a.V - v0 : p.piece), n_ct = (n_v + kHlTile - 1) / kHlTile;
+    const int n_rp = (p.Rp + p.bn - 1) / p.bn;
+    hipLaunchKernelGGL((k_hl_grad<TI, TJ, WRN>), dim3((unsigned)((n_ct + 7) / 8 * 8 * n_rp)), dim3(kThreads), 0, st, a,
+                       (int)v0, n_v, n_rp);
+    if (a.d_hidden)
+      hipLaunchKernelGGL((k_hl_dhidden<TI, TJ, WRN>), dim3((unsigned)(n_dt * n_rt * p.n_split)), dim3(kThreads), 0, st,
+                         a, (int)v0, n_v, n_rt, n_dt, v0 > 0 ? 1 : 0);
+    if (a.d_weight)
+      hipLaunchKernelGGL(k_hl_dweight, dim3((unsigned)(n_dt * n_ct)), dim3(kThreads), 0, st, a, (int)v0, n_v, n_dt);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.d_hidden) {
+    const int64_t n4 = (int64_t)a.R * (a.D / 4);
+    hipLaunchKernelGGL(k_hl_reduce, dim3((unsigned)((n4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_head_loss(const HlArgs& a, hipStream_t st) {
+  if (a.plan.bn == 64) return head_loss<2, 2, 4>(a, st);
+  if (a.plan.bn == 128) return head_loss<4, 2, 2>(a, st);
+  return head_loss<4, 4, 2>(a, st);
+}
+
+}  // namespace specv

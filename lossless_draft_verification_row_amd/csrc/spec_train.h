@@ -1,0 +1,112 @@
+// spec_train.h -- launch descriptors of the drafter-training operators: the top logits of a row,
+// distillation from them, and the LM head's cross entropy with its gradient.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace specv {
+
+// ---------------------------------------------------------------- LM head cross entropy
+
+constexpr int kHlTile = 256;      // vocabulary columns (and features) per tile
+constexpr int kHlDepth = 64;      // k per stage
+
+struct HlRow {                    // what the gradient tiles need of a row
+  float lz2;                      // log2 sum 2^(l c)
+  float scale;                    // row weight / T; 0: the row is left out
+  int y;                          // target, -1: none
+  int pad;
+};
+
+// How a call is cut up; the same on the host for the workspace's size and for the launches.
+struct HlPlan {
+  int Rp;                         // rows rounded up to whole stages (the gradient tiles' k)
+  int n_ct;                       // vocabulary tiles
+  int bn;                         // rows per tile: 64, 128 or 256
+  int piece;                      // vocabulary columns whose logit gradients are held at a time
+  int n_split;                    // parts of a piece's k in the product for the hidden states' gradient
+};
+
+struct HlArgs {
+  const uint16_t* hidden;         // [R, D] bf16, row stride h_ld
+  int64_t h_ld;
+  const uint16_t* weight;         // [V, D] bf16, row stride w_ld
+  int64_t w_ld;
+  int R, V, D;
+  float c;                        // log2(e) / T
+  double inv_t;
+  const int32_t* targets;         // [R]
+  const float* row_weight;        // [R] or nullptr (1)
+  float* loss;                    // [R]
+  float* log_z;                   // [R] or nullptr
+  uint16_t* d_hidden;             // [R, D] bf16, row stride dh_ld, or nullptr
+  int64_t dh_ld;
+  uint16_t* d_weight;             // [V, D] bf16, row stride dw_ld, or nullptr
+  int64_t dw_ld;
+  HlPlan plan;
+  float2* rec;                    // [n_ct][Rp]: a tile's maximum of a row and sum of 2^((l - m) c)
+  float* ly;                      // [Rp]: the target's logit
+  HlRow* rows;                    // [Rp]
+  uint16_t* hz;                   // [Rp][D]: the hidden rows, those left out zeroed
+  uint16_t* g;                    // [Rp][piece]: dL/dl of the piece at hand, bf16
+  float* part;                    // [n_split][Rp][D]: parts of the hidden states' gradient
+};
+
+hipError_t launch_head_loss(const HlArgs& a, hipStream_t st);
+hipError_t launch_head_zero(uint16_t* d_weight, int64_t ld, int V, int D, hipStream_t st);
+
+// ---------------------------------------------------------------- top logits, distillation
+
+constexpr int kTrSeg = 8192;      // logits of one workgroup (32 per thread)
+constexpr int kTrMaxK = 256;      // longest list
+constexpr int kTrMaxV = 1 << 21;  // largest vocabulary
+
+struct MaxSum {                   // a part of a row: its maximum and sum of 2^((l - m) c)
+  float m, s;
+};
+
+struct TopkArgs {
+  const void* logits;             // [R, V], row stride ld
+  int64_t ld;
+  int R, V, K, n_seg, cap;
+  float c;                        // log2(e) / T
+  double inv_t;
+  int32_t* index;                 // [R, K]
+  float* logit;                   // [R, K]
+  float* log_z;                   // [R] or nullptr
+  uint64_t* cand;                 // [R][n_seg][cap]: order key and complemented index
+  int32_t* n_cand;                // [R][n_seg]; -1: the segment holds a NaN or +inf
+  MaxSum* ms;                     // [R][n_seg]
+};
+// Candidates that a segment may hand on: its K largest always fit.
+inline int topk_cap(int K) { return (K + K / 2 + 32 + 15) & ~15; }
+hipError_t launch_row_topk(const TopkArgs& a, int dt, int vec, hipStream_t st);
+
+struct DistillRow {               // what the gradient needs of a row
+  float m, f;                     // d = 2^((l - m) c) f outside the list
+  int zero;                       // the row's gradient is zero
+  int pad;
+};
+struct DistillArgs {
+  const void* logits;             // [R, V] student rows, row stride ld
+  int64_t ld;
+  int R, V, K, n_seg;
+  float c;                        // log2(e) / T
+  double inv_t;
+  const int32_t* index;           // [R, K] teacher's tokens
+  const float* teacher;           // [R, K] their logits
+  const float* teacher_log_z;     // [R] or nullptr: the list is renormalised
+  const float* row_weight;        // [R] or nullptr (1)
+  float* loss;                    // [R]
+  float* log_z;                   // [R] or nullptr
+  void* d_logits;                 // [R, V], row stride d_ld, of the logits' type, or nullptr; may be `logits`
+  int64_t d_ld;
+  MaxSum* ms;                     // [R][n_seg]: the logits outside the list
+  DistillRow* rows;               // [R]
+  float* d_list;                  // [R][K]: the gradient at the list's tokens
+};
+hipError_t launch_topk_distill(const DistillArgs& a, int dt, int vec, hipStream_t st);
+
+}  // namespace specv

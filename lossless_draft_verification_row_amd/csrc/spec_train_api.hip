@@ -1,0 +1,260 @@
+// spec_train_api.hip -- the C ABI of the drafter-training operators: argument checks, workspace
+// carving, launches.  Declarations and their documentation are in include/spec_verify.h.
+#include <limits.h>
+#include <math.h>
+#include <string.h>
+
+#include "spec_device.h"
+#include "spec_train.h"
+#include "spec_verify.h"
+
+using namespace specv;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int kMaxRows = 1 << 22;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+struct Carve {
+  char* base;
+  size_t off = 0;
+  template <typename T>
+  T* take(size_t bytes) {
+    T* p = base ? (T*)(base + off) : nullptr;
+    off += align_up(bytes);
+    return p;
+  }
+};
+
+int elem_bytes(spec_dtype dt) { return dt == SPEC_BF16 ? 2 : 4; }
+// A C caller's enum may hold any int, which is looked at as such.
+bool dtype_valid(const spec_dtype& dt) {
+  int v;
+  static_assert(sizeof(v) == sizeof(dt), "a C enum");
+  memcpy(&v, &dt, sizeof(v));
+  return v == SPEC_BF16 || v == SPEC_F32;
+}
+bool rows16(const void* p, int64_t ld, int elem) { return ((uintptr_t)p % 16) == 0 && (ld * elem) % 16 == 0; }
+bool temperature_valid(float t) { return t > 0.f && isfinite(t) && isfinite(1.f / t); }
+float exp2_scale(float t) { return (float)(1.4426950408889634 / (double)t); }
+int n_segments(int V) { return (V + kTrSeg - 1) / kTrSeg; }
+
+HlPlan hl_plan(int R, int V, int D) {
+  HlPlan p;
+  p.Rp = (int)(((int64_t)R + kHlDepth - 1) / kHlDepth * kHlDepth);
+  p.n_ct = (int)(((int64_t)V + kHlTile - 1) / kHlTile);
+  p.bn = R <= 64 ? 64 : R <= 128 ? 128 : 256;
+  // G of a piece within 256 MB (one tile's columns at least): the memory-side cache's size
+  const int64_t cols = ((int64_t)1 << 27) / p.Rp / kHlTile * kHlTile;
+  const int64_t all = (int64_t)p.n_ct * kHlTile;
+  p.piece = (int)(cols < kHlTile ? kHlTile : cols < all ? cols : all);
+  // parts of the product for d_hidden: one tile per CU, each at least eight stages long
+  const int64_t tiles = (((int64_t)R + p.bn - 1) / p.bn) * (((int64_t)D + kHlTile - 1) / kHlTile);
+  int64_t s = 256 / tiles;
+  const int64_t most = p.piece / (8 * kHlDepth);
+  s = s > most ? most : s;
+  p.n_split = (int)(s < 1 ? 1 : s);
+  return p;
+}
+
+// Every carve is done twice: with a null base for the size, with the workspace for the call.
+void carve_topk(Carve& cv, TopkArgs& a) {
+  const size_t n = (size_t)a.R * a.n_seg;
+  a.cand = cv.take<uint64_t>(n * a.cap * sizeof(uint64_t));
+  a.n_cand = cv.take<int32_t>(n * sizeof(int32_t));
+  a.ms = cv.take<MaxSum>(n * sizeof(MaxSum));
+}
+void carve_distill(Carve& cv, DistillArgs& a, bool grad) {
+  a.ms = cv.take<MaxSum>((size_t)a.R * a.n_seg * sizeof(MaxSum));
+  if (!grad) return;
+  a.rows = cv.take<DistillRow>((size_t)a.R * sizeof(DistillRow));
+  a.d_list = cv.take<float>((size_t)a.R * a.K * sizeof(float));
+}
+void carve_head(Carve& cv, HlArgs& a, bool grad) {
+  const HlPlan& p = a.plan;
+  a.rec = cv.take<float2>((size_t)p.n_ct * p.Rp * sizeof(float2));
+  a.ly = cv.take<float>((size_t)p.Rp * sizeof(float));
+  a.rows = cv.take<HlRow>((size_t)p.Rp * sizeof(HlRow));
+  if (!grad) return;
+  a.hz = cv.take<uint16_t>((size_t)p.Rp * a.D * sizeof(uint16_t));
+  a.g = cv.take<uint16_t>((size_t)p.Rp * p.piece * sizeof(uint16_t));
+  a.part = cv.take<float>((size_t)p.n_split * p.Rp * a.D * sizeof(float));
+}
+bool head_sizes_valid(int R, int V, int D) {
+  return R >= 0 && V > 0 && D > 0 && R <= kMaxRows && V <= kTrMaxV && D <= kTrMaxV;
+}
+
+// A workspace that a call can use: enough bytes, on the alignment its arrays are carved at.
+int check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need) return SPEC_ERR_WORKSPACE;
+  return ((uintptr_t)ws % kAlign) == 0 ? SPEC_OK : SPEC_ERR_INVALID;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_row_topk_workspace_bytes(int R, int V, int K) {
+  if (R <= 0 || V <= 0 || K <= 0 || R > kMaxRows || V > kTrMaxV || K > kTrMaxK) return 0;
+  TopkArgs a;
+  memset(&a, 0, sizeof(a));
+  a.R = R;
+  a.n_seg = n_segments(V);
+  a.cap = topk_cap(K);
+  Carve cv{nullptr};
+  carve_topk(cv, a);
+  return cv.off;
+}
+
+int spec_row_topk(int R, int V, int K, spec_dtype dt, const void* logits, int64_t ld, float temperature,
+                  int32_t* out_index, float* out_logit, float* out_log_z, void* workspace, size_t workspace_bytes,
+                  void* hip_stream) {
+  if (R < 0 || V <= 0 || K <= 0 || !dtype_valid(dt) || !temperature_valid(temperature)) return SPEC_ERR_INVALID;
+  if (V > kTrMaxV || K > kTrMaxK || R > kMaxRows) return SPEC_ERR_UNSUPPORTED;
+  if (R == 0) return SPEC_OK;
+  if (!logits || ld < V || !out_index || !out_logit) return SPEC_ERR_INVALID;
+  if ((int64_t)R * n_segments(V) > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  const int ws = check_workspace(workspace, workspace_bytes, spec_row_topk_workspace_bytes(R, V, K));
+  if (ws != SPEC_OK) return ws;
+  TopkArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.ld = ld;
+  a.R = R;
+  a.V = V;
+  a.K = K;
+  a.n_seg = n_segments(V);
+  a.cap = topk_cap(K);
+  a.c = exp2_scale(temperature);
+  a.inv_t = 1.0 / (double)temperature;
+  a.index = out_index;
+  a.logit = out_logit;
+  a.log_z = out_log_z;
+  Carve cv{(char*)workspace};
+  carve_topk(cv, a);
+  const hipError_t e = launch_row_topk(a, dt == SPEC_BF16 ? kDtBF16 : kDtF32, rows16(logits, ld, elem_bytes(dt)) ? 1 : 0,
+                                       (hipStream_t)hip_stream);
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+}
+
+size_t spec_topk_distill_workspace_bytes(int R, int V, int K, int grad) {
+  if (R <= 0 || V <= 0 || K <= 0 || R > kMaxRows || V > kTrMaxV || K > kTrMaxK) return 0;
+  DistillArgs a;
+  memset(&a, 0, sizeof(a));
+  a.R = R;
+  a.K = K;
+  a.n_seg = n_segments(V);
+  Carve cv{nullptr};
+  carve_distill(cv, a, grad != 0);
+  return cv.off;
+}
+
+int spec_topk_distill(int R, int V, int K, spec_dtype dt, const void* logits, int64_t ld, const int32_t* index,
+                      const float* teacher_logit, const float* teacher_log_z, float temperature,
+                      const float* row_weight, float* out_loss, float* out_log_z, void* d_logits, int64_t d_ld,
+                      void* workspace, size_t workspace_bytes, void* hip_stream) {
+  if (R < 0 || V <= 0 || K <= 0 || !dtype_valid(dt) || !temperature_valid(temperature)) return SPEC_ERR_INVALID;
+  if (V > kTrMaxV || K > kTrMaxK || R > kMaxRows) return SPEC_ERR_UNSUPPORTED;
+  if (R == 0) return SPEC_OK;
+  if (!logits || ld < V || !index || !teacher_logit || !out_loss) return SPEC_ERR_INVALID;
+  if (d_logits && d_ld < V) return SPEC_ERR_INVALID;
+  // in place: every logit and its gradient share their place, so the rows must too
+  if (d_logits == logits && d_ld != ld) return SPEC_ERR_INVALID;
+  if ((int64_t)R * n_segments(V) > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  const int ws = check_workspace(workspace, workspace_bytes, spec_topk_distill_workspace_bytes(R, V, K, d_logits != nullptr));
+  if (ws != SPEC_OK) return ws;
+  DistillArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.ld = ld;
+  a.R = R;
+  a.V = V;
+  a.K = K;
+  a.n_seg = n_segments(V);
+  a.c = exp2_scale(temperature);
+  a.inv_t = 1.0 / (double)temperature;
+  a.index = index;
+  a.teacher = teacher_logit;
+  a.teacher_log_z = teacher_log_z;
+  a.row_weight = row_weight;
+  a.loss = out_loss;
+  a.log_z = out_log_z;
+  a.d_logits = d_logits;
+  a.d_ld = d_ld;
+  Carve cv{(char*)workspace};
+  carve_distill(cv, a, d_logits != nullptr);
+  const int es = elem_bytes(dt);
+  const int vec = rows16(logits, ld, es) && (!d_logits || rows16(d_logits, d_ld, es)) ? 1 : 0;
+  const hipError_t e = launch_topk_distill(a, dt == SPEC_BF16 ? kDtBF16 : kDtF32, vec, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+}
+
+size_t spec_lm_head_loss_workspace_bytes(int R, int V, int D, int grad) {
+  if (!head_sizes_valid(R, V, D) || R == 0) return 0;
+  HlArgs a;
+  memset(&a, 0, sizeof(a));
+  a.D = D;
+  a.plan = hl_plan(R, V, D);
+  Carve cv{nullptr};
+  carve_head(cv, a, grad != 0);
+  return cv.off;
+}
+
+int spec_lm_head_loss(int R, int V, int D, const void* hidden, int64_t h_ld, const void* weight, int64_t w_ld,
+                      const int32_t* targets, float temperature, const float* row_weight, float* out_loss,
+                      float* out_log_z, void* d_hidden, int64_t dh_ld, void* d_weight, int64_t dw_ld,
+                      void* workspace, size_t workspace_bytes, void* hip_stream) {
+  if (R < 0 || V <= 0 || D <= 0 || !temperature_valid(temperature)) return SPEC_ERR_INVALID;
+  if (!head_sizes_valid(R, V, D)) return SPEC_ERR_UNSUPPORTED;
+  if (R == 0) {   // no positions: the head's gradient is zero
+    if (!d_weight) return SPEC_OK;
+    if (dw_ld < D) return SPEC_ERR_INVALID;
+    if (D % 8 != 0 || !rows16(d_weight, dw_ld, 2)) return SPEC_ERR_UNSUPPORTED;
+    return launch_head_zero((uint16_t*)d_weight, dw_ld, V, D, (hipStream_t)hip_stream) == hipSuccess ? SPEC_OK
+                                                                                                     : SPEC_ERR_LAUNCH;
+  }
+  if (!hidden || !weight || !targets || !out_loss || h_ld < D || w_ld < D) return SPEC_ERR_INVALID;
+  if ((d_hidden && dh_ld < D) || (d_weight && dw_ld < D)) return SPEC_ERR_INVALID;
+  // the gradients are written while the inputs are still read
+  if ((d_hidden && (d_hidden == hidden || d_hidden == d_weight)) || (d_weight && d_weight == weight)) return SPEC_ERR_INVALID;
+  // 16-byte rows: D, the strides and the bases are whole multiples of eight bf16
+  if (D % 8 != 0 || !rows16(hidden, h_ld, 2) || !rows16(weight, w_ld, 2)) return SPEC_ERR_UNSUPPORTED;
+  if ((d_hidden && !rows16(d_hidden, dh_ld, 2)) || (d_weight && !rows16(d_weight, dw_ld, 2))) return SPEC_ERR_UNSUPPORTED;
+  // a tile's rows are addressed with 32-bit byte offsets (256 rows x stride x 2 B < 2^31)
+  if (h_ld > kTrMaxV || w_ld > kTrMaxV) return SPEC_ERR_UNSUPPORTED;
+  HlArgs a;
+  memset(&a, 0, sizeof(a));
+  a.hidden = (const uint16_t*)hidden;
+  a.h_ld = h_ld;
+  a.weight = (const uint16_t*)weight;
+  a.w_ld = w_ld;
+  a.R = R;
+  a.V = V;
+  a.D = D;
+  a.c = exp2_scale(temperature);
+  a.inv_t = 1.0 / (double)temperature;
+  a.targets = targets;
+  a.row_weight = row_weight;
+  a.loss = out_loss;
+  a.log_z = out_log_z;
+  a.d_hidden = (uint16_t*)d_hidden;
+  a.dh_ld = dh_ld;
+  a.d_weight = (uint16_t*)d_weight;
+  a.dw_ld = dw_ld;
+  a.plan = hl_plan(R, V, D);
+  const int64_t n_rt = ((int64_t)a.plan.Rp + a.plan.bn - 1) / a.plan.bn, n_dt = (D + kHlTile - 1) / kHlTile;
+  if ((a.plan.n_ct + 8) * (n_rt > n_dt ? n_rt : n_dt) > INT_MAX || n_rt * n_dt * a.plan.n_split > INT_MAX ||
+      (int64_t)R * D / 4 > (int64_t)INT_MAX * kThreads || (int64_t)V * D / 8 > (int64_t)INT_MAX * kThreads)
+    return SPEC_ERR_UNSUPPORTED;
+  const bool grad = d_hidden || d_weight;
+  const int ws = check_workspace(workspace, workspace_bytes, spec_lm_head_loss_workspace_bytes(R, V, D, grad));
+  if (ws != SPEC_OK) return ws;
+  Carve cv{(char*)workspace};
+  carve_head(cv, a, grad);
+  const hipError_t e = launch_head_loss(a, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+}
+
+}  // extern "C"

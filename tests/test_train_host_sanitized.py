@@ -1,0 +1,63 @@
+"""The drafter-training entry points' host layer (spec_train_api.hip) built for the CPU under
+AddressSanitizer and UndefinedBehaviorSanitizer with stand-in launchers (tests/native/): workspace
+sizes, carving and every refusal.  No GPU and no kernel are involved."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import lossless_draft_verification_row_amd as L
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+CSRC = os.path.join(ROOT, "lossless_draft_verification_row_amd", "csrc")
+SANITIZE = "-Xarch_host -fsanitize=address,undefined -Xarch_host -fno-sanitize-recover=all".split()
+
+
+def test_training_host_layer_under_sanitizers(tmp_path):
+    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    exe = str(tmp_path / "host_train_check")
+    cmd = [hipcc, "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", *SANITIZE,
+           f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}", f"-I{os.path.join(HERE, 'native')}",
+           "--cuda-host-only", "-x", "hip", os.path.join(CSRC, "spec_train_api.hip"),
+           os.path.join(HERE, "native", "host_stubs.cpp"), os.path.join(HERE, "native", "host_train_check.cpp"), "-o", exe]
+    b = subprocess.run(cmd, capture_output=True, text=True)
+    assert b.returncode == 0, b.stdout + b.stderr
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=1", UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
+    r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert " 0 failures" in r.stdout
+
+
+def test_workspace_sizes_of_the_training_operators():
+    assert L.spec_row_topk_workspace_bytes(0, 100, 4) == 0
+    assert L.spec_row_topk_workspace_bytes(2, 100, 4) > 0
+    assert L.spec_row_topk_workspace_bytes(2, 100, 257) == 0        # a call would be refused
+    a, b = (L.spec_topk_distill_workspace_bytes(8, 151936, 64, g) for g in (False, True))
+    assert 0 < a < b < 1 << 20
+    # the loss alone needs a record per row and tile; with gradients one piece of the logits' gradient,
+    # far from all of it (4096 x 151,936 x 2 B = 1.2 GB)
+    f, g = (L.spec_lm_head_loss_workspace_bytes(4096, 151936, 4096, x) for x in (False, True))
+    assert f < 24 << 20 and g < 500 << 20
+
+
+def test_cpu_tensors_are_refused():
+    l = torch.zeros((2, 10))
+    idx, t = torch.zeros((2, 3), dtype=torch.int32), torch.zeros((2, 3))
+    h = torch.zeros((2, 8), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        L.spec_row_topk(l, 3)
+    with pytest.raises(ValueError):
+        L.spec_topk_distill(l, idx, t)
+    with pytest.raises(ValueError):
+        L.spec_lm_head_loss(h, h, torch.zeros(2, dtype=torch.int32))
+
+
+def test_unknown_types_are_refused():
+    lib = L.load_library()
+    for dt in (-1, 2, 7):
+        assert lib.spec_row_topk(2, 10, 2, dt, 256, 10, 1.0, 256, 256, None, 256, 1 << 20, None) == -1
+        assert lib.spec_topk_distill(2, 10, 2, dt, 256, 10, 256, 256, None, 1.0, None, 256, None, None, 0, 256, 1 << 20, None) == -1
