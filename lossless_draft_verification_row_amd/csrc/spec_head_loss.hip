@@ -47,10 +47,17 @@ struct HlOperand {
 constexpr int kGran = kHlDepth / 8;    // 16-byte granules of a k-contiguous row per stage
 constexpr int kFarOffset = 0x7ffffff0;
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t stage_rsrc(const HlOperand& o, int64_t skip) {
-  const int64_t left = o.bytes - skip;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t stage_rsrc(const HlOperand& o, int64_t skip, int64_t past) {
+  const int64_t left = o.bytes - skip - past;
   const int n = left < 0 ? 0 : left > (int64_t)kFarOffset ? kFarOffset : (int)left;
   return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)o.p + skip), (short)0, n, 0x00020000);
+}
+
+// Wait until at most N of this wave's vector memory accesses are in flight.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N < 64, "a six-bit counter");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4 | 15 << 8);
 }
 
 // Within a k-contiguous row the granules are permuted by an XOR of the row's low bits, within a
@@ -61,17 +68,29 @@ __device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 1);
 // Tile product core: acc[i][j] += A rows (32 (TI wr + i) ..) x B rows (32 (TJ wc + j) ..), A and B
 // 256 and BN rows wide, four waves as WRN x (4 / WRN).  The 32x32x16 MFMA's C has the A row in
 // the element (8 (e / 4) + 4 (lane / 32) + e % 4) and the B row in the lane (lane % 32).
+//
+// Two stage buffers filled by the buffer load's LDS form.  The fragments of k step h + 1 are read
+// while step h's MFMAs run; at a stage's last step every fragment of the stage has been read, so
+// one barrier there both frees its buffer for the loads of the stage after next and, with the
+// wait before it, hands over the next stage, whose first fragments are read under the last
+// step's MFMAs: no LDS latency is left uncovered at a stage's edge, and a stage's loads have a
+// whole stage's time to land.
 template <int TI, int TJ, int WRN, bool KMA, bool KMB>
 struct HlCore {
   static constexpr int WCN = kWaves / WRN;
   static constexpr int BN = 32 * TJ * WCN;
   static constexpr int NA = kHlTile * kGran / kThreads;   // granules per thread and stage
   static constexpr int NB = BN * kGran / kThreads;
+  static constexpr int kSteps = kHlDepth / 16;
+  static constexpr int kReads = TI * (KMA ? 2 : 1) + TJ * (KMB ? 2 : 1);   // LDS reads per step
+  // reads behind each MFMA: all of them within the first half of a step's MFMAs, so that the next
+  // step's first one finds its operands there
+  static constexpr int kRate = (2 * kReads + TI * TJ - 1) / (TI * TJ);
   static_assert(32 * TI * WRN == kHlTile, "A is 256 rows wide");
   static_assert(!KMB || BN == kHlTile, "a k-major B is 256 rows wide");
-  struct Lds {
-    uint4 a[2][kHlTile * kGran];
-    uint4 b[2][BN * kGran];
+  struct Buf {
+    uint4 a[kHlTile * kGran];
+    uint4 b[BN * kGran];
   };
 
   // byte offset within a stage of the granule that this thread's load n fills
@@ -99,68 +118,128 @@ struct HlCore {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t)&lds[64 * (N * wave + n)], 16, off, 0, 0, 0);
     }
   }
-  // fragment of 32 rows from `row0`, k 16 h .. 16 h + 15 of the stage
+  // This lane's byte offsets within a stage's operand, of which the fragment reads differ by
+  // constants only: k contiguous, one per k step; k major, one per 32-row block.
   template <bool KM>
-  static __device__ __forceinline__ bf16x8 frag(const uint4* lds, int row0, int h, int lane) {
+  static __device__ __forceinline__ void frag_offsets(int row0, int lane, int (&o)[4]) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if constexpr (KM) {
+        // each 16 lanes read a 4 (k) x 16 (rows) block transposed: lane q of them addresses k q / 4,
+        // rows 4 (q % 4) .., and receives row q's four k
+        const int q = lane & 15, g = row0 / 8 + 4 * x + 2 * ((lane >> 4) & 1) + ((q & 3) >> 1);
+        o[x] = 16 * ((8 * (lane >> 5) + (q >> 2)) * 32 + (g ^ (4 * (q >> 2)))) + 8 * (q & 1);
+      } else {
+        const int r = row0 + (lane & 31);   // swz_row(r + 32 i) is swz_row(r)
+        o[x] = 16 * (r * kGran + ((2 * x + (lane >> 5)) ^ swz_row(r)));
+      }
+    }
+  }
+  // fragment of 32-row block i, k step h
+  template <bool KM>
+  static __device__ __forceinline__ bf16x8 frag(const uint4* lds, const int (&o)[4], int i, int h) {
     if constexpr (KM) {
-      // each 16 lanes read a 4 (k) x 16 (rows) block transposed: lane q of them addresses k q / 4,
-      // rows 4 (q % 4) .., and receives row q's four k
-      const int q = lane & 15, g = row0 / 8 + 2 * ((lane >> 4) & 1) + ((q & 3) >> 1);
-      const int k = 16 * h + 8 * (lane >> 5) + (q >> 2);
-      const char* p = (const char*)lds + 16 * (k * 32 + (g ^ (4 * (q >> 2)))) + 8 * (q & 1);
+      const char* p = (const char*)lds + o[i] + 16 * 512 * h;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)(p + 4 * 512));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const int r = row0 + (lane & 31);
-      return __builtin_bit_cast(bf16x8, lds[r * kGran + ((2 * h + (lane >> 5)) ^ swz_row(r))]);
+      return *(const bf16x8*)((const char*)lds + o[h] + 32 * 16 * kGran * i);
     }
   }
 
-  // n_k stages; k_len (of a k-contiguous operand) beyond which k reads as zero
-  static __device__ __forceinline__ void run(Lds& L, const HlOperand& A, const HlOperand& B, int n_k, int k_len,
-                                             f32x16 (&acc)[TI][TJ]) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wr = wave / WCN, wc = wave % WCN;
-    const int64_t sa = (KMA ? kHlDepth * A.ld : kHlDepth) * 2, sb = (KMB ? kHlDepth * B.ld : kHlDepth) * 2;
+  struct Wave {
+    int lane, wave;
+    int64_t sa, sb;                // bytes from one stage to the next
     int va[NA], vb[NB];
+    int oa[4], ob[4];
+  };
+  static __device__ __forceinline__ void load_stage(Buf& b, const HlOperand& A, const HlOperand& B, const Wave& w, int s,
+                                                    int n_k, int k_len) {
+    // (a stage past the last one: an empty resource, which loads nothing)
+    const int64_t past = s < n_k ? 0 : (int64_t)1 << 62;
+    load<KMA, NA>(b.a, stage_rsrc(A, s * w.sa, past), w.va, w.wave, w.lane, k_len - kHlDepth * s);
+    load<KMB, NB>(b.b, stage_rsrc(B, s * w.sb, past), w.vb, w.wave, w.lane, k_len - kHlDepth * s);
+  }
+  static __device__ __forceinline__ void read(const Buf& b, const Wave& w, int h, bf16x8 (&fa)[TI], bf16x8 (&fb)[TJ]) {
 #pragma unroll
-    for (int n = 0; n < NA; ++n) va[n] = load_offset<KMA, NA>(n, wave, lane, A.ld);
+    for (int j = 0; j < TJ; ++j) fb[j] = frag<KMB>(b.b, w.ob, j, h);
 #pragma unroll
-    for (int n = 0; n < NB; ++n) vb[n] = load_offset<KMB, NB>(n, wave, lane, B.ld);
+    for (int i = 0; i < TI; ++i) fa[i] = frag<KMA>(b.a, w.oa, i, h);
+  }
+  static __device__ __forceinline__ void mfma(const bf16x8 (&fa)[TI], const bf16x8 (&fb)[TJ], f32x16 (&acc)[TI][TJ]) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+  }
+
+  // Stage s from `cur`; the loads of stage s + 2 go into it once it has been read.
+  static __device__ __forceinline__ void stage(Buf& cur, Buf& next, const HlOperand& A, const HlOperand& B, const Wave& w,
+                                               int s, int n_k, int k_len, bf16x8 (&fa)[2][TI], bf16x8 (&fb)[2][TJ],
+                                               f32x16 (&acc)[TI][TJ]) {
+#pragma unroll
+    for (int h = 0; h < kSteps - 1; ++h) {
+      read(cur, w, h + 1, fa[(h + 1) & 1], fb[(h + 1) & 1]);
+      mfma(fa[h & 1], fb[h & 1], acc);
+#pragma unroll
+      for (int q = 0; q < TI * TJ; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+        if (q * kRate < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kRate, 0);   // LDS reads
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // this wave's loads of stage s + 1 have landed and its reads of stage s are done, and after
+    // the barrier everyone's
+    wait_vmem();
+    __syncthreads();
+    read(next, w, 0, fa[0], fb[0]);
+    load_stage(cur, A, B, w, s + 2, n_k, k_len);
+    mfma(fa[(kSteps - 1) & 1], fb[(kSteps - 1) & 1], acc);
+#pragma unroll
+    for (int q = 0; q < TI * TJ; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (q * kRate < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kRate, 0);
+      if (q < NA + NB) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // global load
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // n_k stages (an odd number is followed by one of zeros); k_len (of a k-contiguous operand)
+  // beyond which k reads as zero
+  static __device__ __forceinline__ void run(Buf& b0, Buf& b1, const HlOperand& A, const HlOperand& B, int n_k, int k_len,
+                                             f32x16 (&acc)[TI][TJ]) {
+    Wave w;
+    w.lane = threadIdx.x & 63;
+    w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    w.sa = (KMA ? kHlDepth * A.ld : kHlDepth) * 2;
+    w.sb = (KMB ? kHlDepth * B.ld : kHlDepth) * 2;
+#pragma unroll
+    for (int n = 0; n < NA; ++n) w.va[n] = load_offset<KMA, NA>(n, w.wave, w.lane, A.ld);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) w.vb[n] = load_offset<KMB, NB>(n, w.wave, w.lane, B.ld);
+    frag_offsets<KMA>(32 * TI * (w.wave / WCN), w.lane, w.oa);
+    frag_offsets<KMB>(32 * TJ * (w.wave % WCN), w.lane, w.ob);
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-    load<KMA, NA>(L.a[0], stage_rsrc(A, 0), va, wave, lane, k_len);
-    load<KMB, NB>(L.b[0], stage_rsrc(B, 0), vb, wave, lane, k_len);
-    for (int s = 0; s < n_k; ++s) {
-      // this wave's loads of stage s have landed, and after the barrier everyone's; every wave is
-      // also done with the other buffer, which the next stage's loads now fill
-      wait_vmem();
-      __syncthreads();
-      if (s + 1 < n_k) {
-        load<KMA, NA>(L.a[(s + 1) & 1], stage_rsrc(A, (s + 1) * sa), va, wave, lane, k_len - kHlDepth * (s + 1));
-        load<KMB, NB>(L.b[(s + 1) & 1], stage_rsrc(B, (s + 1) * sb), vb, wave, lane, k_len - kHlDepth * (s + 1));
-      }
-      const uint4 *la = L.a[s & 1], *lb = L.b[s & 1];
-#pragma unroll
-      for (int h = 0; h < kHlDepth / 16; ++h) {
-        bf16x8 fa[TI], fb[TJ];
-#pragma unroll
-        for (int i = 0; i < TI; ++i) fa[i] = frag<KMA>(la, 32 * (TI * wr + i), h, lane);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) fb[j] = frag<KMB>(lb, 32 * (TJ * wc + j), h, lane);
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-          for (int j = 0; j < TJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-      }
+    load_stage(b0, A, B, w, 0, n_k, k_len);
+    load_stage(b1, A, B, w, 1, n_k, k_len);
+    wait_vm<NA + NB>();   // stage 0's loads
+    __builtin_amdgcn_s_barrier();
+    bf16x8 fa[2][TI], fb[2][TJ];
+    read(b0, w, 0, fa[0], fb[0]);
+    // two stages a turn, so that either buffer is known where it is read or loaded: the compiler
+    // makes an LDS read wait for every load in flight into what it may alias
+    for (int s = 0; s < n_k; s += 2) {
+      stage(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
+      stage(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
     }
-    wait_vmem();       // (without a stage: the first one's loads)
+    wait_vmem();
     __syncthreads();   // every wave is done with the stage buffers
   }
 };
@@ -215,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void k_hl_prep(HlArgs a, int grad) {
 template <int TI, int TJ, int WRN>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_stats(HlArgs a, int n_rt) {
   using Core = HlCore<TI, TJ, WRN, false, false>;
-  __shared__ typename Core::Lds L;
+  __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
   const int jx = blockIdx.x >> 3, rt = jx % n_rt, ct = (jx / n_rt) * 8 + (blockIdx.x & 7);
@@ -224,12 +303,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   f32x16 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
   const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
-  Core::run(L, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
+  Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
 
   // A lane holds 16 TI columns of TJ rows; lane ^ 32 holds the rows' other columns of this wave,
   // the other WRN - 1 waves those of the tile.  -inf keeps its weight 0; a NaN or +inf logit makes
   // the sum NaN (inf - inf), also where it is all that a lane holds.
-  float2* part = (float2*)&L;   // [WRN][BN]
+  float2* part = (float2*)&b0;   // [WRN][BN]
   const int vl = v0 + 32 * TI * wr + 4 * (lane >> 5);
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
@@ -316,7 +395,7 @@ template <int TI, int TJ, int WRN>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_grad(HlArgs a, int pv0,
                                                                                                 int n_v, int n_rt) {
   using Core = HlCore<TI, TJ, WRN, false, false>;
-  __shared__ typename Core::Lds L;
+  __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
   const int jx = blockIdx.x >> 3, rt = jx % n_rt, ct = (jx / n_rt) * 8 + (blockIdx.x & 7);
@@ -325,7 +404,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   f32x16 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
   const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
-  Core::run(L, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
+  Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
   const int n_vp = (n_v + kHlDepth - 1) / kHlDepth * kHlDepth;
   const int vt = 32 * TI * wr + 4 * (lane >> 5);      // the lane's first column within the tile
 #pragma unroll
@@ -358,7 +437,7 @@ template <int TI, int TJ, int WRN>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_dhidden(
     HlArgs a, int pv0, int n_v, int n_rt, int n_dt, int add) {
   using Core = HlCore<TI, TJ, WRN, true, false>;
-  __shared__ typename Core::Lds L;
+  __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
   const int dt = blockIdx.x % n_dt, rt = blockIdx.x / n_dt % n_rt, sp = blockIdx.x / n_dt / n_rt;
@@ -372,7 +451,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
                        extent(a.V, a.D, a.w_ld, pv0 + k0, d0)};
   const HlOperand B = {a.g + (int64_t)r0 * a.plan.piece + k0, a.plan.piece,
                        extent(a.plan.Rp, a.plan.piece, a.plan.piece, r0, k0)};
-  Core::run(L, A, B, s1 - s0, (s1 - s0) * kHlDepth, acc);
+  Core::run(b0, b1, A, B, s1 - s0, (s1 - s0) * kHlDepth, acc);
   float* part = a.part + (int64_t)sp * a.plan.Rp * a.D;
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
@@ -401,7 +480,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
                                                                                                    int n_v, int n_dt) {
   constexpr int TI = 4, TJ = 4, WRN = 2;
   using Core = HlCore<TI, TJ, WRN, true, true>;
-  __shared__ typename Core::Lds L;
+  __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
   const int dt = blockIdx.x % n_dt, ct = blockIdx.x / n_dt;
@@ -409,7 +488,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   f32x16 acc[TI][TJ];
   const HlOperand A = {a.hz + d0, a.D, extent(a.plan.Rp, a.D, a.D, 0, d0)};
   const HlOperand B = {a.g + vt0, a.plan.piece, extent(a.plan.Rp, a.plan.piece, a.plan.piece, 0, vt0)};
-  Core::run(L, A, B, a.plan.Rp / kHlDepth, a.plan.Rp, acc);
+  Core::run(b0, b1, A, B, a.plan.Rp / kHlDepth, a.plan.Rp, acc);
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
     const int vl = vt0 + 32 * (TJ * wc + j) + (lane & 31);
