@@ -154,11 +154,13 @@ struct HlCore {
     int va[NA], vb[NB];
     int oa[4], ob[4];
   };
-  static __device__ __forceinline__ void load_stage(Buf& b, const HlOperand& A, const HlOperand& B, const Wave& w, int s,
-                                                    int n_k, int k_len) {
-    // (a stage past the last one: an empty resource, which loads nothing)
+  // (a stage past the last one: an empty resource, which loads nothing)
+  static __device__ __forceinline__ void load_a(Buf& b, const HlOperand& A, const Wave& w, int s, int n_k, int k_len) {
     const int64_t past = s < n_k ? 0 : (int64_t)1 << 62;
     load<KMA, NA>(b.a, stage_rsrc(A, s * w.sa, past), w.va, w.wave, w.lane, k_len - kHlDepth * s);
+  }
+  static __device__ __forceinline__ void load_b(Buf& b, const HlOperand& B, const Wave& w, int s, int n_k, int k_len) {
+    const int64_t past = s < n_k ? 0 : (int64_t)1 << 62;
     load<KMB, NB>(b.b, stage_rsrc(B, s * w.sb, past), w.vb, w.wave, w.lane, k_len - kHlDepth * s);
   }
   static __device__ __forceinline__ void read(const Buf& b, const Wave& w, int h, bf16x8 (&fa)[TI], bf16x8 (&fb)[TJ]) {
@@ -182,26 +184,29 @@ struct HlCore {
 #pragma unroll
     for (int h = 0; h < kSteps - 1; ++h) {
       read(cur, w, h + 1, fa[(h + 1) & 1], fb[(h + 1) & 1]);
+      if (h == 0) load_b(next, B, w, s + 1, n_k, k_len);
       mfma(fa[h & 1], fb[h & 1], acc);
-#pragma unroll
-      for (int q = 0; q < TI * TJ; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
-        if (q * kRate < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kRate, 0);   // LDS reads
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      order<NB>(h == 0);
     }
     // this wave's loads of stage s + 1 have landed and its reads of stage s are done, and after
     // the barrier everyone's
     wait_vmem();
     __syncthreads();
     read(next, w, 0, fa[0], fb[0]);
-    load_stage(cur, A, B, w, s + 2, n_k, k_len);
+    load_a(cur, A, w, s + 2, n_k, k_len);
     mfma(fa[(kSteps - 1) & 1], fb[(kSteps - 1) & 1], acc);
+    order<NA>(true);
+  }
+  // The order of a step: behind each MFMA kRate reads as long as there are any, and with `loads`
+  // every second time one of N loads.
+  template <int N>
+  static __device__ __forceinline__ void order(bool loads) {
+    constexpr int kGap = TI * TJ / N > 0 ? TI * TJ / N : 1, kLoads = (N + TI * TJ - 1) / (TI * TJ);
 #pragma unroll
     for (int q = 0; q < TI * TJ; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (q * kRate < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kRate, 0);
-      if (q < NA + NB) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // global load
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+      if (q * kRate < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kRate, 0);   // LDS reads
+      if (loads && q % kGap == 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);   // global loads
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -227,9 +232,10 @@ struct HlCore {
       for (int j = 0; j < TJ; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-    load_stage(b0, A, B, w, 0, n_k, k_len);
-    load_stage(b1, A, B, w, 1, n_k, k_len);
-    wait_vm<NA + NB>();   // stage 0's loads
+    load_a(b0, A, w, 0, n_k, k_len);
+    load_b(b0, B, w, 0, n_k, k_len);
+    load_a(b1, A, w, 1, n_k, k_len);
+    wait_vm<NA>();   // stage 0's loads
     __builtin_amdgcn_s_barrier();
     bf16x8 fa[2][TI], fb[2][TJ];
     read(b0, w, 0, fa[0], fb[0]);
@@ -247,6 +253,21 @@ struct HlCore {
 // What lies between element (row, col) of a [rows, cols] matrix and the end of its last row.
 __device__ __forceinline__ int64_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t row, int64_t col) {
   return ((rows - 1 - row) * ld + cols - col) * 2;
+}
+
+// Which of the n_in x n_out tiles this workgroup takes.  Workgroup i runs on XCD i mod 8; each XCD
+// takes a contiguous run of the tiles in an order of blocks, 8 outer ones wide, of 4 inner x 8
+// outer tiles: the 32 workgroups that an XCD runs at a time share 12 operand strips in its L2
+// (18 in an order of 16 inner x 2 outer ones), and an outer strip is done with once its block is.
+__device__ __forceinline__ void tile_of(int u, int n_in, int n_out, int& in, int& out) {
+  const int ob = u / (8 * n_in), rem = u - ob * 8 * n_in, ow = min(8, n_out - 8 * ob);
+  const int g = rem / (4 * ow), w = rem - g * 4 * ow, gs = min(4, n_in - 4 * g);
+  in = 4 * g + w % gs;
+  out = 8 * ob + w / gs;
+}
+__device__ __forceinline__ int xcd_run(int n) {
+  const int x = blockIdx.x & 7;
+  return x * (n >> 3) + min(x, n & 7) + (int)(blockIdx.x >> 3);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -297,8 +318,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
-  const int jx = blockIdx.x >> 3, rt = jx % n_rt, ct = (jx / n_rt) * 8 + (blockIdx.x & 7);
-  if (ct >= a.plan.n_ct) return;
+  int rt, ct;
+  tile_of(xcd_run(gridDim.x), n_rt, a.plan.n_ct, rt, ct);
   const int v0 = ct * kHlTile, r0 = rt * Core::BN;
   f32x16 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
@@ -398,8 +419,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
-  const int jx = blockIdx.x >> 3, rt = jx % n_rt, ct = (jx / n_rt) * 8 + (blockIdx.x & 7);
-  if (ct * kHlTile >= n_v) return;
+  int rt, ct;
+  tile_of(xcd_run(gridDim.x), n_rt, (n_v + kHlTile - 1) / kHlTile, rt, ct);
   const int v0 = pv0 + ct * kHlTile, r0 = rt * Core::BN;
   f32x16 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
@@ -440,7 +461,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
-  const int dt = blockIdx.x % n_dt, rt = blockIdx.x / n_dt % n_rt, sp = blockIdx.x / n_dt / n_rt;
+  const int u = xcd_run(gridDim.x), sp = u / (n_dt * n_rt);
+  int dt, rt;
+  tile_of(u - sp * n_dt * n_rt, n_dt, n_rt, dt, rt);
   const int d0 = dt * kHlTile, r0 = rt * Core::BN;
   // this split's stages of the piece
   const int n_st = (n_v + kHlDepth - 1) / kHlDepth;
@@ -483,7 +506,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
-  const int dt = blockIdx.x % n_dt, ct = blockIdx.x / n_dt;
+  int dt, ct;
+  tile_of(xcd_run(gridDim.x), n_dt, (n_v + kHlTile - 1) / kHlTile, dt, ct);
   const int d0 = dt * kHlTile, vt0 = ct * kHlTile;
   f32x16 acc[TI][TJ];
   const HlOperand A = {a.hz + d0, a.D, extent(a.plan.Rp, a.D, a.D, 0, d0)};
@@ -539,7 +563,7 @@ hipError_t head_loss(const HlArgs& a, hipStream_t st) {
   const bool grad = a.d_hidden || a.d_weight;
   const int n_rt = (a.R + p.bn - 1) / p.bn, n_dt = (a.D + kHlTile - 1) / kHlTile;
   hipLaunchKernelGGL(k_hl_prep, dim3((unsigned)((p.Rp + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a, grad ? 1 : 0);
-  hipLaunchKernelGGL((k_hl_stats<TI, TJ, WRN>), dim3((unsigned)((p.n_ct + 7) / 8 * 8 * n_rt)), dim3(kThreads), 0, st, a,
+  hipLaunchKernelGGL((k_hl_stats<TI, TJ, WRN>), dim3((unsigned)(p.n_ct * n_rt)), dim3(kThreads), 0, st, a,
                      n_rt);
   hipLaunchKernelGGL(k_hl_rows, dim3((unsigned)((a.R + 15) / 16)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
@@ -547,7 +571,7 @@ hipError_t head_loss(const HlArgs& a, hipStream_t st) {
   for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
     const int n_v = (int)(a.V - v0 < p.piece ? a.V - v0 : p.piece), n_ct = (n_v + kHlTile - 1) / kHlTile;
     const int n_rp = (p.Rp + p.bn - 1) / p.bn;
-    hipLaunchKernelGGL((k_hl_grad<TI, TJ, WRN>), dim3((unsigned)((n_ct + 7) / 8 * 8 * n_rp)), dim3(kThreads), 0, st, a,
+    hipLaunchKernelGGL((k_hl_grad<TI, TJ, WRN>), dim3((unsigned)(n_ct * n_rp)), dim3(kThreads), 0, st, a,
                        (int)v0, n_v, n_rp);
     if (a.d_hidden)
       hipLaunchKernelGGL((k_hl_dhidden<TI, TJ, WRN>), dim3((unsigned)(n_dt * n_rt * p.n_split)), dim3(kThreads), 0, st,
