@@ -28,7 +28,7 @@ namespace specv {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_void_t;
 typedef __attribute__((address_space(3))) s16x4* lds_s4_t;
@@ -61,33 +61,37 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 // Within a k-contiguous row the granules are permuted by an XOR of the row's low bits, within a
-// k-major row (one k, all rows of the tile) by 4 (k % 4), so that a fragment read's phases fall
+// k-major row (one k, all rows of the tile) by one of k's, so that a fragment read's phases fall
 // into distinct banks.
 __device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swz_k(int k) { return 4 * (k & 3) ^ 2 * ((k >> 3) & 1); }
 
-// Tile product core: acc[i][j] += A rows (32 (TI wr + i) ..) x B rows (32 (TJ wc + j) ..), A and B
-// 256 and BN rows wide, four waves as WRN x (4 / WRN).  The 32x32x16 MFMA's C has the A row in
-// the element (8 (e / 4) + 4 (lane / 32) + e % 4) and the B row in the lane (lane % 32).
+// Tile product core: acc[i][j] += A rows (16 (TI wr + i) ..) x B rows (16 (TJ wc + j) ..), A and B
+// 256 and BN rows wide, four waves as WRN x (4 / WRN).  The 16x16x32 MFMA's A and B have the row
+// in lane % 16 and k in 8 (lane / 16) + element; its C has the A row in 4 (lane / 16) + element
+// and the B row in lane % 16.  (With operands that change the matrix cores sustain 1.81 PFLOP/s
+// on this shape and 1.57 on 32x32x16, which moves more accumulator bytes per product: the power
+// that the data costs sets the rate.)
 //
-// Two stage buffers filled by the buffer load's LDS form.  The fragments of k step h + 1 are read
-// while step h's MFMAs run; at a stage's last step every fragment of the stage has been read, so
-// one barrier there both frees its buffer for the loads of the stage after next and, with the
-// wait before it, hands over the next stage, whose first fragments are read under the last
-// step's MFMAs: no LDS latency is left uncovered at a stage's edge, and a stage's loads have a
-// whole stage's time to land.
+// Two stage buffers filled by the buffer load's LDS form.  A step's MFMAs go row by row (one A
+// fragment against all of B's); behind each row the A fragment that it used is read again for
+// the next step, and B's next fragments into a second set, so that no LDS latency is uncovered.
+// One barrier a stage, two rows into its last step: every read of the stage's buffer was issued
+// before those rows, so that the wait for them is covered, and so is the waves' skew.  It frees
+// the buffer for the loads of the stage after next and, with the wait before it, hands over the
+// next stage.  A stage's loads are spread over a step's time (their addresses take the texture
+// unit 16 cycles each: in a burst the loads of four waves would hold up the MFMAs behind them)
+// and have more than a step's time to land.
 template <int TI, int TJ, int WRN, bool KMA, bool KMB>
 struct HlCore {
   static constexpr int WCN = kWaves / WRN;
-  static constexpr int BN = 32 * TJ * WCN;
+  static constexpr int BN = 16 * TJ * WCN;
   static constexpr int NA = kHlTile * kGran / kThreads;   // granules per thread and stage
   static constexpr int NB = BN * kGran / kThreads;
-  static constexpr int kSteps = kHlDepth / 16;
-  static constexpr int kReads = TI * (KMA ? 2 : 1) + TJ * (KMB ? 2 : 1);   // LDS reads per step
-  // reads behind each MFMA: all of them within the first half of a step's MFMAs, so that the next
-  // step's first one finds its operands there
-  static constexpr int kRate = (2 * kReads + TI * TJ - 1) / (TI * TJ);
-  static_assert(32 * TI * WRN == kHlTile, "A is 256 rows wide");
+  static constexpr int kSteps = kHlDepth / 32;
+  static_assert(16 * TI * WRN == kHlTile, "A is 256 rows wide");
   static_assert(!KMB || BN == kHlTile, "a k-major B is 256 rows wide");
+  static_assert(TI <= 8 && TJ <= 8 && kSteps == 2, "fragment offsets");
   struct Buf {
     uint4 a[kHlTile * kGran];
     uint4 b[BN * kGran];
@@ -98,7 +102,7 @@ struct HlCore {
   static __device__ __forceinline__ int load_offset(int n, int wave, int lane, int64_t ld) {
     const int p = 64 * (N * wave + n) + lane;
     if constexpr (KM) {
-      const int k = p >> 5, g = (p & 31) ^ (4 * (k & 3));
+      const int k = p >> 5, g = (p & 31) ^ swz_k(k);
       return (int)(k * ld * 2) + 16 * g;
     } else {
       const int r = p >> 3, g = (p & 7) ^ swz_row(r);
@@ -106,115 +110,155 @@ struct HlCore {
     }
   }
   template <bool KM, int N>
-  static __device__ __forceinline__ void load(uint4* lds, __amdgpu_buffer_rsrc_t rs, const int (&v)[N], int wave,
+  static __device__ __forceinline__ void load(uint4* lds, __amdgpu_buffer_rsrc_t rs, const int (&v)[N], int n, int wave,
                                               int lane, int k_left) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      int off = v[n];
-      if constexpr (!KM) {   // a granule past the row's end reads as zero
-        const int p = 64 * (N * wave + n) + lane;
-        if (8 * ((p & 7) ^ swz_row(p >> 3)) >= k_left) off = kFarOffset;
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t)&lds[64 * (N * wave + n)], 16, off, 0, 0, 0);
+    int off = v[n];
+    if constexpr (!KM) {   // a granule past the row's end reads as zero
+      const int p = 64 * (N * wave + n) + lane;
+      if (8 * ((p & 7) ^ swz_row(p >> 3)) >= k_left) off = kFarOffset;
     }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t)&lds[64 * (N * wave + n)], 16, off, 0, 0, 0);
   }
   // This lane's byte offsets within a stage's operand, of which the fragment reads differ by
-  // constants only: k contiguous, one per k step; k major, one per 32-row block.
+  // constants only: k contiguous, one per k step; k major, one per 16-row block.
   template <bool KM>
-  static __device__ __forceinline__ void frag_offsets(int row0, int lane, int (&o)[4]) {
+  static __device__ __forceinline__ void frag_offsets(int row0, int lane, int (&o)[8]) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < 8; ++x) {
       if constexpr (KM) {
         // each 16 lanes read a 4 (k) x 16 (rows) block transposed: lane q of them addresses k q / 4,
         // rows 4 (q % 4) .., and receives row q's four k
-        const int q = lane & 15, g = row0 / 8 + 4 * x + 2 * ((lane >> 4) & 1) + ((q & 3) >> 1);
-        o[x] = 16 * ((8 * (lane >> 5) + (q >> 2)) * 32 + (g ^ (4 * (q >> 2)))) + 8 * (q & 1);
+        const int q = lane & 15, k = 8 * (lane >> 4) + (q >> 2), g = row0 / 8 + 2 * x + ((q & 3) >> 1);
+        o[x] = 16 * (k * 32 + (g ^ swz_k(k))) + 8 * (q & 1);   // k + 4 and k + 32 have k's XOR
       } else {
-        const int r = row0 + (lane & 31);   // swz_row(r + 32 i) is swz_row(r)
-        o[x] = 16 * (r * kGran + ((2 * x + (lane >> 5)) ^ swz_row(r)));
+        const int r = row0 + (lane & 15);   // swz_row(r + 16 i) is swz_row(r)
+        o[x] = 16 * (r * kGran + ((4 * (x & 1) + (lane >> 4)) ^ swz_row(r)));
       }
     }
   }
-  // fragment of 32-row block i, k step h
+  // fragment of 16-row block i, k step h
   template <bool KM>
-  static __device__ __forceinline__ bf16x8 frag(const uint4* lds, const int (&o)[4], int i, int h) {
+  static __device__ __forceinline__ bf16x8 frag(const uint4* lds, const int (&o)[8], int i, int h) {
     if constexpr (KM) {
-      const char* p = (const char*)lds + o[i] + 16 * 512 * h;
+      const char* p = (const char*)lds + o[i] + 32 * 512 * h;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)(p + 4 * 512));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      return *(const bf16x8*)((const char*)lds + o[h] + 32 * 16 * kGran * i);
+      return *(const bf16x8*)((const char*)lds + o[h] + 16 * 16 * kGran * i);
     }
   }
+
+  // acc += a b in place.  Written out so that the accumulators stay where they are: given the
+  // choice, the register allocator moves them between the halves of a full register file at
+  // every step.  Nothing but MFMAs touches them inside the loop; settle() is what must pass
+  // before their first other use.
+  static __device__ __forceinline__ void mma(f32x4& c, const bf16x8& a, const bf16x8& b) {
+    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  }
+  static __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
   struct Wave {
     int lane, wave;
     int64_t sa, sb;                // bytes from one stage to the next
     int va[NA], vb[NB];
-    int oa[4], ob[4];
+    int oa[8], ob[8];
   };
-  // (a stage past the last one: an empty resource, which loads nothing)
-  static __device__ __forceinline__ void load_a(Buf& b, const HlOperand& A, const Wave& w, int s, int n_k, int k_len) {
+  // Loads n0 .. n1 - 1 of stage s (A's, then B's); a stage past the last one has an empty resource,
+  // which loads nothing.
+  static __device__ __forceinline__ void loads(Buf& b, const HlOperand& A, const HlOperand& B, const Wave& w, int s,
+                                               int n_k, int k_len, int n0, int n1) {
     const int64_t past = s < n_k ? 0 : (int64_t)1 << 62;
-    load<KMA, NA>(b.a, stage_rsrc(A, s * w.sa, past), w.va, w.wave, w.lane, k_len - kHlDepth * s);
-  }
-  static __device__ __forceinline__ void load_b(Buf& b, const HlOperand& B, const Wave& w, int s, int n_k, int k_len) {
-    const int64_t past = s < n_k ? 0 : (int64_t)1 << 62;
-    load<KMB, NB>(b.b, stage_rsrc(B, s * w.sb, past), w.vb, w.wave, w.lane, k_len - kHlDepth * s);
-  }
-  static __device__ __forceinline__ void read(const Buf& b, const Wave& w, int h, bf16x8 (&fa)[TI], bf16x8 (&fb)[TJ]) {
+    const __amdgpu_buffer_rsrc_t ra = stage_rsrc(A, s * w.sa, past), rb = stage_rsrc(B, s * w.sb, past);
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) fb[j] = frag<KMB>(b.b, w.ob, j, h);
-#pragma unroll
-    for (int i = 0; i < TI; ++i) fa[i] = frag<KMA>(b.a, w.oa, i, h);
+    for (int n = 0; n < NA + NB; ++n) {
+      if (n < n0 || n >= n1) continue;
+      if (n < NA) load<KMA, NA>(b.a, ra, w.va, n, w.wave, w.lane, k_len - kHlDepth * s);
+      else load<KMB, NB>(b.b, rb, w.vb, n - NA, w.wave, w.lane, k_len - kHlDepth * s);
+    }
   }
-  static __device__ __forceinline__ void mfma(const bf16x8 (&fa)[TI], const bf16x8 (&fb)[TJ], f32x16 (&acc)[TI][TJ]) {
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-  }
+  static constexpr int kHold = 2;                                  // rows of step 1 before the barrier
+  static constexpr int kRowLoads = (NA + NB + TI - 1) / TI;        // loads behind one row of MFMAs
+  static constexpr int kReadRows = TI - kHold < 4 ? TI - kHold : 4;   // rows behind which B's reads go
+  static constexpr int kRowB = TJ / kReadRows;
+  static_assert(kRowB * kReadRows == TJ, "whole rows of B reads");
 
-  // Stage s from `cur`; the loads of stage s + 2 go into it once it has been read.
-  static __device__ __forceinline__ void stage(Buf& cur, Buf& next, const HlOperand& A, const HlOperand& B, const Wave& w,
-                                               int s, int n_k, int k_len, bf16x8 (&fa)[2][TI], bf16x8 (&fb)[2][TJ],
-                                               f32x16 (&acc)[TI][TJ]) {
+  // One row of MFMAs with fragment reads (task 0 .. NT - 1) and loads (0 .. NL - 1) placed evenly
+  // between them; each MFMA and what follows it is a scheduling region of its own.
+  template <int I, int NT, int NL, typename Task, typename Load>
+  static __device__ __forceinline__ void row(const bf16x8 (&fa)[TI], const bf16x8 (&fb)[TJ], f32x4 (&acc)[TI][TJ],
+                                             Task task, Load ld) {
 #pragma unroll
-    for (int h = 0; h < kSteps - 1; ++h) {
-      read(cur, w, h + 1, fa[(h + 1) & 1], fb[(h + 1) & 1]);
-      if (h == 0) load_b(next, B, w, s + 1, n_k, k_len);
-      mfma(fa[h & 1], fb[h & 1], acc);
-      order<NB>(h == 0);
+    for (int j = 0; j < TJ; ++j) {
+      mma(acc[I][j], fa[I], fb[j]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t * TJ / NT == j) task(t);
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+        if (l * TJ / NL == j) ld(l);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    // this wave's loads of stage s + 1 have landed and its reads of stage s are done, and after
-    // the barrier everyone's
-    wait_vmem();
-    __syncthreads();
-    read(next, w, 0, fa[0], fb[0]);
-    load_a(cur, A, w, s + 2, n_k, k_len);
-    mfma(fa[(kSteps - 1) & 1], fb[(kSteps - 1) & 1], acc);
-    order<NA>(true);
   }
-  // The order of a step: behind each MFMA kRate reads as long as there are any, and with `loads`
-  // every second time one of N loads.
-  template <int N>
-  static __device__ __forceinline__ void order(bool loads) {
-    constexpr int kGap = TI * TJ / N > 0 ? TI * TJ / N : 1, kLoads = (N + TI * TJ - 1) / (TI * TJ);
-#pragma unroll
-    for (int q = 0; q < TI * TJ; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
-      if (q * kRate < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kRate, 0);   // LDS reads
-      if (loads && q % kGap == 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);   // global loads
+  // Rows I .. of step 0: the previous row's A fragment and some of B's are read for step 1, and
+  // the last of stage s + 1's loads go out.
+  template <int I>
+  static __device__ __forceinline__ void rows0(Buf& cur, Buf& next, const HlOperand& A, const HlOperand& B, const Wave& w,
+                                               int s, int n_k, int k_len, bf16x8 (&fa)[TI], bf16x8 (&fb)[2][TJ],
+                                               f32x4 (&acc)[TI][TJ]) {
+    if constexpr (I < TI) {
+      constexpr int n0 = (TI - kHold + I) * kRowLoads, n1 = n0 + kRowLoads < NA + NB ? n0 + kRowLoads : NA + NB;
+      constexpr int nl = I < kHold && n1 > n0 ? n1 - n0 : 0, nb = I < kReadRows ? kRowB : 0;
+      row<I, 1 + nb, nl>(
+          fa, fb[0], acc,
+          [&](int t) {
+            if (t == 0) {
+              if constexpr (I == 0) fa[TI - 1] = frag<KMA>(cur.a, w.oa, TI - 1, 0);
+              else fa[I - 1] = frag<KMA>(cur.a, w.oa, I - 1, 1);
+            } else {
+              fb[1][kRowB * I + t - 1] = frag<KMB>(cur.b, w.ob, kRowB * I + t - 1, 1);
+            }
+          },
+          [&](int l) { loads(next, A, B, w, s + 1, n_k, k_len, n0 + l, n0 + l + 1); });
+      rows0<I + 1>(cur, next, A, B, w, s, n_k, k_len, fa, fb, acc);
     }
-    __builtin_amdgcn_sched_barrier(0);
+  }
+  // Rows I .. of step 1: from row kHold on the next stage's first fragments are read and this
+  // buffer is loaded with stage s + 2.
+  template <int I>
+  static __device__ __forceinline__ void rows1(Buf& cur, Buf& next, const HlOperand& A, const HlOperand& B, const Wave& w,
+                                               int s, int n_k, int k_len, bf16x8 (&fa)[TI], bf16x8 (&fb)[2][TJ],
+                                               f32x4 (&acc)[TI][TJ]) {
+    if constexpr (I < TI) {
+      if constexpr (I == kHold) {
+        // this wave's loads of stage s + 1 have landed and its reads of stage s are done, and
+        // after the barrier everyone's
+        wait_vmem();
+        __syncthreads();
+      }
+      constexpr int n0 = (I - kHold) * kRowLoads, n1 = n0 + kRowLoads < NA + NB ? n0 + kRowLoads : NA + NB;
+      constexpr int nl = I >= kHold && n1 > n0 ? n1 - n0 : 0, ib = I - kHold, nb = ib >= 0 && ib < kReadRows ? kRowB : 0;
+      constexpr int na = I == 0 ? 1 : I == kHold ? kHold : I > kHold ? 1 : 0;
+      row<I, na + nb, nl>(
+          fa, fb[1], acc,
+          [&](int t) {
+            if (t < na) {
+              if constexpr (I == 0) fa[TI - 1] = frag<KMA>(cur.a, w.oa, TI - 1, 1);
+              else if constexpr (I == kHold) fa[t] = frag<KMA>(next.a, w.oa, t, 0);
+              else fa[I - 1] = frag<KMA>(next.a, w.oa, I - 1, 0);
+            } else {
+              fb[0][kRowB * ib + t - na] = frag<KMB>(next.b, w.ob, kRowB * ib + t - na, 0);
+            }
+          },
+          [&](int l) { loads(cur, A, B, w, s + 2, n_k, k_len, n0 + l, n0 + l + 1); });
+      rows1<I + 1>(cur, next, A, B, w, s, n_k, k_len, fa, fb, acc);
+    }
   }
 
   // n_k stages (an odd number is followed by one of zeros); k_len (of a k-contiguous operand)
   // beyond which k reads as zero
   static __device__ __forceinline__ void run(Buf& b0, Buf& b1, const HlOperand& A, const HlOperand& B, int n_k, int k_len,
-                                             f32x16 (&acc)[TI][TJ]) {
+                                             f32x4 (&acc)[TI][TJ]) {
     Wave w;
     w.lane = threadIdx.x & 63;
     w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -224,27 +268,33 @@ struct HlCore {
     for (int n = 0; n < NA; ++n) w.va[n] = load_offset<KMA, NA>(n, w.wave, w.lane, A.ld);
 #pragma unroll
     for (int n = 0; n < NB; ++n) w.vb[n] = load_offset<KMB, NB>(n, w.wave, w.lane, B.ld);
-    frag_offsets<KMA>(32 * TI * (w.wave / WCN), w.lane, w.oa);
-    frag_offsets<KMB>(32 * TJ * (w.wave % WCN), w.lane, w.ob);
+    frag_offsets<KMA>(16 * TI * (w.wave / WCN), w.lane, w.oa);
+    frag_offsets<KMB>(16 * TJ * (w.wave % WCN), w.lane, w.ob);
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-    load_a(b0, A, w, 0, n_k, k_len);
-    load_b(b0, B, w, 0, n_k, k_len);
-    load_a(b1, A, w, 1, n_k, k_len);
-    wait_vm<NA>();   // stage 0's loads
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+    constexpr int kFirst = (TI - kHold) * kRowLoads < NA + NB ? (TI - kHold) * kRowLoads : NA + NB;
+    loads(b0, A, B, w, 0, n_k, k_len, 0, NA + NB);
+    loads(b1, A, B, w, 1, n_k, k_len, 0, kFirst);
+    wait_vm<kFirst>();   // stage 0's loads
     __builtin_amdgcn_s_barrier();
-    bf16x8 fa[2][TI], fb[2][TJ];
-    read(b0, w, 0, fa[0], fb[0]);
+    bf16x8 fa[TI], fb[2][TJ];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) fb[0][j] = frag<KMB>(b0.b, w.ob, j, 0);
+#pragma unroll
+    for (int i = 0; i < TI - 1; ++i) fa[i] = frag<KMA>(b0.a, w.oa, i, 0);
     // two stages a turn, so that either buffer is known where it is read or loaded: the compiler
     // makes an LDS read wait for every load in flight into what it may alias
     for (int s = 0; s < n_k; s += 2) {
-      stage(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
-      stage(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
+      rows0<0>(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
+      rows1<0>(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
+      rows0<0>(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
+      rows1<0>(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
     }
+    settle();
     wait_vmem();
     __syncthreads();   // every wave is done with the stage buffers
   }
@@ -321,46 +371,50 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   int rt, ct;
   tile_of(xcd_run(gridDim.x), n_rt, a.plan.n_ct, rt, ct);
   const int v0 = ct * kHlTile, r0 = rt * Core::BN;
-  f32x16 acc[TI][TJ];
+  f32x4 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
   const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
   Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
 
-  // A lane holds 16 TI columns of TJ rows; lane ^ 32 holds the rows' other columns of this wave,
-  // the other WRN - 1 waves those of the tile.  -inf keeps its weight 0; a NaN or +inf logit makes
-  // the sum NaN (inf - inf), also where it is all that a lane holds.
+  // A lane holds 4 TI columns of TJ rows; the lanes 16, 32 and 48 on hold the rows' other columns
+  // of this wave, the other WRN - 1 waves those of the tile.  -inf keeps its weight 0; a NaN or
+  // +inf logit makes the sum NaN (inf - inf), also where it is all that a lane holds.
   float2* part = (float2*)&b0;   // [WRN][BN]
-  const int vl = v0 + 32 * TI * wr + 4 * (lane >> 5);
+  const int vl = v0 + 16 * TI * wr + 4 * (lane >> 4);
+  if (v0 + kHlTile > a.V) {   // the vocabulary's last tile
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (vl + 16 * i + e >= a.V)
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) acc[i][j][e] = -INFINITY;
+  }
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
-    if (v0 + kHlTile > a.V) {   // the vocabulary's last tile
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          acc[i][j][e] = vl + 32 * i + 8 * (e >> 2) + (e & 3) < a.V ? acc[i][j][e] : -INFINITY;
-    }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
+    m = fmaxf(m, __shfl_xor(m, 16));
     m = fmaxf(m, __shfl_xor(m, 32));
     float s = 0.f;
     if (m > -INFINITY) {
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * a.c);
+        for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * a.c);
     } else {
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < 4; ++e)
           if (acc[i][j][e] != acc[i][j][e]) s = acc[i][j][e];
     }
+    s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (lane < 32) part[wr * Core::BN + 32 * (TJ * wc + j) + lane] = make_float2(m, s);
+    if (lane < 16) part[wr * Core::BN + 16 * (TJ * wc + j) + lane] = make_float2(m, s);
   }
   __syncthreads();
   for (int t = threadIdx.x; t < Core::BN; t += kThreads) {
@@ -422,34 +476,32 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   int rt, ct;
   tile_of(xcd_run(gridDim.x), n_rt, (n_v + kHlTile - 1) / kHlTile, rt, ct);
   const int v0 = pv0 + ct * kHlTile, r0 = rt * Core::BN;
-  f32x16 acc[TI][TJ];
+  f32x4 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
   const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
   Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
   const int n_vp = (n_v + kHlDepth - 1) / kHlDepth * kHlDepth;
-  const int vt = 32 * TI * wr + 4 * (lane >> 5);      // the lane's first column within the tile
+  const int vt = 16 * TI * wr + 4 * (lane >> 4);      // the lane's first column within the tile
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
-    const int r = r0 + 32 * (TJ * wc + j) + (lane & 31);
+    const int r = r0 + 16 * (TJ * wc + j) + (lane & 15);
     if (r >= a.plan.Rp) continue;
     const HlRow row = a.rows[r];
     uint16_t* g = a.g + (int64_t)r * a.plan.piece + ct * kHlTile;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = 0; i < TI; ++i) {
+      const int v = vt + 16 * i;
+      float x[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int v = vt + 32 * i + 8 * q;
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + e], a.c, -row.lz2));
-          x[e] = (v0 + v + e == row.y ? p - 1.f : p) * row.scale;
-          if (row.scale == 0.f || v0 + v + e >= a.V) x[e] = 0.f;
-        }
-        // G is rounded to bf16 (half a step, 2^-9 of each entry): both products take bf16
-        // operands, and the errors of a row's entries are independent
-        if (ct * kHlTile + v < n_vp) *(uint2*)(g + v) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      for (int e = 0; e < 4; ++e) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], a.c, -row.lz2));
+        x[e] = (v0 + v + e == row.y ? p - 1.f : p) * row.scale;
+        if (row.scale == 0.f || v0 + v + e >= a.V) x[e] = 0.f;
       }
+      // G is rounded to bf16 (half a step, 2^-9 of each entry): both products take bf16
+      // operands, and the errors of a row's entries are independent
+      if (ct * kHlTile + v < n_vp) *(uint2*)(g + v) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    }
   }
 }
 
@@ -469,7 +521,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   const int n_st = (n_v + kHlDepth - 1) / kHlDepth;
   const int s0 = (int)((int64_t)n_st * sp / a.plan.n_split), s1 = (int)((int64_t)n_st * (sp + 1) / a.plan.n_split);
   const int k0 = s0 * kHlDepth;
-  f32x16 acc[TI][TJ];
+  f32x4 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)(pv0 + k0) * a.w_ld + d0, a.w_ld,
                        extent(a.V, a.D, a.w_ld, pv0 + k0, d0)};
   const HlOperand B = {a.g + (int64_t)r0 * a.plan.piece + k0, a.plan.piece,
@@ -478,30 +530,28 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   float* part = a.part + (int64_t)sp * a.plan.Rp * a.D;
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
-    const int r = r0 + 32 * (TJ * wc + j) + (lane & 31);
+    const int r = r0 + 16 * (TJ * wc + j) + (lane & 15);
     if (r >= a.plan.Rp) continue;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int d = d0 + 32 * (TI * wr + i) + 8 * q + 4 * (lane >> 5);
-        if (d < a.D) {
-          float4* p = (float4*)(part + (int64_t)r * a.D + d);
-          float4 x = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-          if (add) {
-            const float4 o = *p;
-            x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
-          }
-          *p = x;
+    for (int i = 0; i < TI; ++i) {
+      const int d = d0 + 16 * (TI * wr + i) + 4 * (lane >> 4);
+      if (d < a.D) {
+        float4* p = (float4*)(part + (int64_t)r * a.D + d);
+        float4 x = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        if (add) {
+          const float4 o = *p;
+          x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
         }
+        *p = x;
       }
+    }
   }
 }
 
 // dW[v][d] of the piece: k = r, A = h (k major, rows d), B = G (k major, rows v).
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_hl_dweight(HlArgs a, int pv0,
                                                                                                    int n_v, int n_dt) {
-  constexpr int TI = 4, TJ = 4, WRN = 2;
+  constexpr int TI = 8, TJ = 8, WRN = 2;
   using Core = HlCore<TI, TJ, WRN, true, true>;
   __shared__ typename Core::Buf b0, b1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -509,24 +559,21 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   int dt, ct;
   tile_of(xcd_run(gridDim.x), n_dt, (n_v + kHlTile - 1) / kHlTile, dt, ct);
   const int d0 = dt * kHlTile, vt0 = ct * kHlTile;
-  f32x16 acc[TI][TJ];
+  f32x4 acc[TI][TJ];
   const HlOperand A = {a.hz + d0, a.D, extent(a.plan.Rp, a.D, a.D, 0, d0)};
   const HlOperand B = {a.g + vt0, a.plan.piece, extent(a.plan.Rp, a.plan.piece, a.plan.piece, 0, vt0)};
   Core::run(b0, b1, A, B, a.plan.Rp / kHlDepth, a.plan.Rp, acc);
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
-    const int vl = vt0 + 32 * (TJ * wc + j) + (lane & 31);
+    const int vl = vt0 + 16 * (TJ * wc + j) + (lane & 15);
     if (vl >= n_v) continue;
     uint16_t* o = a.d_weight + (int64_t)(pv0 + vl) * a.dw_ld;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int d = d0 + 32 * (TI * wr + i) + 8 * q + 4 * (lane >> 5);
-        if (d < a.D)
-          *(uint2*)(o + d) = make_uint2(pack_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
-                                        pack_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
-      }
+    for (int i = 0; i < TI; ++i) {
+      const int d = d0 + 16 * (TI * wr + i) + 4 * (lane >> 4);
+      if (d < a.D)
+        *(uint2*)(o + d) = make_uint2(pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]));
+    }
   }
 }
 
@@ -591,9 +638,9 @@ hipError_t head_loss(const HlArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_head_loss(const HlArgs& a, hipStream_t st) {
-  if (a.plan.bn == 64) return head_loss<2, 2, 4>(a, st);
-  if (a.plan.bn == 128) return head_loss<4, 2, 2>(a, st);
-  return head_loss<4, 4, 2>(a, st);
+  if (a.plan.bn == 64) return head_loss<4, 4, 4>(a, st);
+  if (a.plan.bn == 128) return head_loss<8, 4, 2>(a, st);
+  return head_loss<8, 8, 2>(a, st);
 }
 
 }  // namespace specv
