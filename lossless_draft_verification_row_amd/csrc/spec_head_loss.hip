@@ -325,6 +325,31 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// A wave's 16 TI columns x 16 TJ rows as bf16 by way of LDS (16 TI bytes x 2 a row, the wave's own
+// 32 TI TJ 16 bytes), so that what it stores are whole rows' pieces of 32 TI bytes: the lanes' own
+// four columns of sixteen rows would be 32-byte pieces.  put(i, j) gives block (i, j)'s four packed
+// columns, row(r) the place of row r's first column or null, n_col the columns that exist (a
+// multiple of 8).
+template <int TI, int TJ, typename Put, typename Row>
+__device__ __forceinline__ void store_rows(uint4* lds, int lane, int n_col, Put put, Row row) {
+  constexpr int kG = 2 * TI;   // 16-byte granules of a row, permuted by an XOR of the row
+#pragma unroll
+  for (int j = 0; j < TJ; ++j)
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int r = 16 * j + (lane & 15), g = 2 * i + (lane >> 5);
+      ((uint2*)&lds[r * kG + (g ^ (r & (kG - 1)))])[(lane >> 4) & 1] = put(i, j);
+    }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int n = 0; n < TJ * 16 * kG / 64; ++n) {
+    const int r = n * (64 / kG) + lane / kG, g = lane % kG;
+    uint16_t* p = row(r);
+    const uint4 x = lds[r * kG + (g ^ (r & (kG - 1)))];
+    if (p && 8 * g < n_col) *(uint4*)(p + 8 * g) = x;
+  }
+}
+
 // One wave per row (rows past R are set up as left out): the target's logit in fp32, the scale
 // of the row's gradient, and the hidden row with a row that is left out zeroed, so that what it
 // holds (padding may be NaN) never meets a product.
@@ -481,28 +506,35 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
   Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
   const int n_vp = (n_v + kHlDepth - 1) / kHlDepth * kHlDepth;
-  const int vt = 16 * TI * wr + 4 * (lane >> 4);      // the lane's first column within the tile
+  const int vw = 16 * TI * wr;                        // the wave's first column within the tile
+  float lz2[TJ], scale[TJ];
+  int y[TJ];                                          // target, from the lane's first column on
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
     const int r = r0 + 16 * (TJ * wc + j) + (lane & 15);
-    if (r >= a.plan.Rp) continue;
-    const HlRow row = a.rows[r];
-    uint16_t* g = a.g + (int64_t)r * a.plan.piece + ct * kHlTile;
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int v = vt + 16 * i;
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], a.c, -row.lz2));
-        x[e] = (v0 + v + e == row.y ? p - 1.f : p) * row.scale;
-        if (row.scale == 0.f || v0 + v + e >= a.V) x[e] = 0.f;
-      }
-      // G is rounded to bf16 (half a step, 2^-9 of each entry): both products take bf16
-      // operands, and the errors of a row's entries are independent
-      if (ct * kHlTile + v < n_vp) *(uint2*)(g + v) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-    }
+    HlRow row = {0.f, 0.f, -1, 0};
+    if (r < a.plan.Rp) row = a.rows[r];
+    lz2[j] = row.lz2;
+    scale[j] = row.scale;
+    y[j] = row.y - (v0 + vw + 4 * (lane >> 4));
   }
+  const int v_left = a.V - (v0 + vw + 4 * (lane >> 4));   // columns that exist from there on
+  uint16_t* g0 = a.g + (int64_t)(r0 + 16 * TJ * wc) * a.plan.piece + ct * kHlTile + vw;
+  store_rows<TI, TJ>(
+      (wave & 2 ? b1.a : b0.a) + (wave & 1) * 32 * TI * TJ, lane, n_vp - ct * kHlTile - vw,
+      [&](int i, int j) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], a.c, -lz2[j]));
+          x[e] = (y[j] == 16 * i + e ? p - 1.f : p) * scale[j];
+          if (scale[j] == 0.f || 16 * i + e >= v_left) x[e] = 0.f;
+        }
+        // G is rounded to bf16 (half a step, 2^-9 of each entry): both products take bf16
+        // operands, and the errors of a row's entries are independent
+        return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      },
+      [&](int r) { return r0 + 16 * TJ * wc + r < a.plan.Rp ? g0 + (int64_t)r * a.plan.piece : nullptr; });
 }
 
 // dh[r][d] over columns of the piece: k = v, A = W (k major, rows d), B = G (k contiguous).
@@ -563,18 +595,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   const HlOperand A = {a.hz + d0, a.D, extent(a.plan.Rp, a.D, a.D, 0, d0)};
   const HlOperand B = {a.g + vt0, a.plan.piece, extent(a.plan.Rp, a.plan.piece, a.plan.piece, 0, vt0)};
   Core::run(b0, b1, A, B, a.plan.Rp / kHlDepth, a.plan.Rp, acc);
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const int vl = vt0 + 16 * (TJ * wc + j) + (lane & 15);
-    if (vl >= n_v) continue;
-    uint16_t* o = a.d_weight + (int64_t)(pv0 + vl) * a.dw_ld;
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int d = d0 + 16 * (TI * wr + i) + 4 * (lane >> 4);
-      if (d < a.D)
-        *(uint2*)(o + d) = make_uint2(pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]));
-    }
-  }
+  const int vw = vt0 + 16 * TJ * wc, dw = d0 + 16 * TI * wr;   // the wave's first row and column
+  uint16_t* o0 = a.d_weight + (int64_t)(pv0 + vw) * a.dw_ld + dw;
+  store_rows<TI, TJ>(
+      (wave & 2 ? b1.a : b0.a) + (wave & 1) * 32 * TI * TJ, lane, a.D - dw,
+      [&](int i, int j) {
+        return make_uint2(pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]));
+      },
+      [&](int r) { return vw + r < n_v ? o0 + r * a.dw_ld : nullptr; });
 }
 
 // d_hidden = the splits' parts, added in order, rounded once.
