@@ -19,6 +19,7 @@
 
 #include "spec_device.h"
 #include "spec_train.h"
+#include "spec_train_device.h"
 
 namespace specv {
 
@@ -26,35 +27,11 @@ constexpr int kTdPer = kTrSeg / kThreads;   // 32 logits per thread
 constexpr double kTdTailMin = 0x1p-20;      // mass off the list that counts: below it is the
                                             // rounding of an fp32 log Z
 
-template <int DT>
-struct TdEl {
-  static constexpr int n = DT == kDtBF16 ? 8 : 4;   // logits of a 16-byte vector
-};
+// Index within the segment of register j of this thread (tr_load's order).
 template <int DT>
 __device__ __forceinline__ int td_index(int j) {
-  constexpr int kEl = TdEl<DT>::n;
+  constexpr int kEl = TrEl<DT>::n;
   return kEl * ((int)threadIdx.x + kThreads * (j / kEl)) + j % kEl;
-}
-template <int DT, bool VEC>
-__device__ __forceinline__ void td_load(const void* row, int V, int base, float (&v)[kTdPer]) {
-  constexpr int kEl = TdEl<DT>::n;
-#pragma unroll
-  for (int q = 0; q < kTdPer / kEl; ++q) {
-    const int e0 = base + td_index<DT>(q * kEl);
-    if (VEC && e0 + kEl <= V) {
-      const uint4 x = ld_nt16((const char*)row + (int64_t)e0 * (16 / kEl));
-      if constexpr (DT == kDtBF16) {
-        v[8 * q + 0] = bf16_lo(x.x); v[8 * q + 1] = bf16_hi(x.x); v[8 * q + 2] = bf16_lo(x.y); v[8 * q + 3] = bf16_hi(x.y);
-        v[8 * q + 4] = bf16_lo(x.z); v[8 * q + 5] = bf16_hi(x.z); v[8 * q + 6] = bf16_lo(x.w); v[8 * q + 7] = bf16_hi(x.w);
-      } else {
-        v[4 * q + 0] = __uint_as_float(x.x); v[4 * q + 1] = __uint_as_float(x.y);
-        v[4 * q + 2] = __uint_as_float(x.z); v[4 * q + 3] = __uint_as_float(x.w);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kEl; ++e) v[kEl * q + e] = e0 + e < V ? logit_at<DT>(row, e0 + e) : -INFINITY;
-    }
-  }
 }
 __device__ __forceinline__ uint32_t td_pack(float a, float b) {
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
@@ -66,13 +43,14 @@ __device__ __forceinline__ void td_put(void* row, int i, float x) {
   if constexpr (DT == kDtBF16) ((__bf16*)row)[i] = (__bf16)x;
   else ((float*)row)[i] = x;
 }
-template <int DT, bool VEC>
-__device__ __forceinline__ void td_store(void* row, int V, int base, const float (&v)[kTdPer]) {
-  constexpr int kEl = TdEl<DT>::n;
+// The first n of a segment's logits to p, in tr_load's order.
+template <int DT>
+__device__ __forceinline__ void td_store(void* p, int n, const float (&v)[kTdPer]) {
+  constexpr int kEl = TrEl<DT>::n;
 #pragma unroll
   for (int q = 0; q < kTdPer / kEl; ++q) {
-    const int e0 = base + td_index<DT>(q * kEl);
-    if (VEC && e0 + kEl <= V) {
+    const int e0 = td_index<DT>(q * kEl);
+    if (e0 + kEl <= n) {
       uint4 x;
       if constexpr (DT == kDtBF16)
         x = make_uint4(td_pack(v[8 * q], v[8 * q + 1]), td_pack(v[8 * q + 2], v[8 * q + 3]),
@@ -80,11 +58,11 @@ __device__ __forceinline__ void td_store(void* row, int V, int base, const float
       else
         x = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
                        __float_as_uint(v[4 * q + 3]));
-      *(uint4*)((char*)row + (int64_t)e0 * (16 / kEl)) = x;
+      st16_any((char*)p + (int64_t)e0 * (16 / kEl), x);
     } else {
 #pragma unroll
       for (int e = 0; e < kEl; ++e)
-        if (e0 + e < V) td_put<DT>(row, e0 + e, v[kEl * q + e]);
+        if (e0 + e < n) td_put<DT>(p, e0 + e, v[kEl * q + e]);
     }
   }
 }
@@ -98,72 +76,63 @@ __device__ __forceinline__ int td_token(const DistillArgs& a, int64_t r, int j, 
   return x >= 0 && x < a.V && t != -INFINITY ? x : -1;
 }
 
-template <int DT, bool VEC>
+template <int DT>
 __global__ __launch_bounds__(kThreads) void k_td_stats(DistillArgs a) {
   __shared__ uint32_t listed[kTrSeg / 32];   // a bit per logit of the segment
-  __shared__ float red[2 * kWaves];
-  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * kTrSeg, t = threadIdx.x;
+  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * a.seg, t = threadIdx.x;
+  constexpr int kEl = TrEl<DT>::n;
   float v[kTdPer];
-  td_load<DT, VEC>(row_ptr<DT>(a.logits, a.ld, r), a.V, base, v);
+  tr_load<DT>((const char*)row_ptr<DT>(a.logits, a.ld, r) + (int64_t)base * (16 / kEl), min(a.seg, a.V - base), v);
   listed[t] = 0;
   __syncthreads();
   float tl;
   const int x = td_token(a, r, t, tl) - base;
-  if (x >= 0 && x < kTrSeg) atomicOr(&listed[x >> 5], 1u << (x & 31));
+  if (x >= 0 && x < a.seg) atomicOr(&listed[x >> 5], 1u << (x & 31));
   __syncthreads();
-  constexpr int kEl = TdEl<DT>::n;
   float m = -INFINITY;
 #pragma unroll
   for (int q = 0; q < kTdPer / kEl; ++q) {
     const int i = td_index<DT>(q * kEl);
-    const uint32_t b = listed[i >> 5] >> (i & 31);
+    const uint32_t b = listed[i >> 5] >> (i & 31) & ((1u << kEl) - 1);
+    if (b)
 #pragma unroll
-    for (int e = 0; e < kEl; ++e) {
-      if (b & (1u << e)) v[kEl * q + e] = -INFINITY;
-      m = fmaxf(m, v[kEl * q + e]);
-    }
-  }
-  m = block_max(m, red);
-  float s = 0.f;
+      for (int e = 0; e < kEl; ++e)
+        if (b & (1u << e)) v[kEl * q + e] = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kTdPer; ++j) {
-    // nothing but -inf (or a NaN, which fmaxf passes over and the sum then shows)
-    const float d = m > -INFINITY ? v[j] - m : v[j];
-    s += __builtin_amdgcn_exp2f(d * a.c);
+    for (int e = 0; e < kEl; ++e) m = fmaxf(m, v[kEl * q + e]);
   }
-  s = wave_sum(s);
-  if ((t & 63) == 0) red[t >> 6] = s;
-  __syncthreads();
-  if (t == 0) a.ms[(int64_t)r * a.n_seg + seg] = MaxSum{m, (red[0] + red[1]) + (red[2] + red[3])};
+  m = wave_max(m);
+  const float s = wave_sum(tr_sum_exp(v, m, a.c));
+  if ((t & 63) == 0) a.ms[((int64_t)r * a.n_seg + seg) * kWaves + (t >> 6)] = MaxSum{m, s};
 }
 
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_td_loss(DistillArgs a) {
-  __shared__ int lx[kTrMaxK];
+  __shared__ alignas(16) int lx[kTrMaxK];
   __shared__ double lp[kTrMaxK];
   __shared__ float red[2 * kWaves];
   __shared__ int redi[2 * kWaves];
   __shared__ double redd[kWaves];
   const int r = blockIdx.x, t = threadIdx.x;
-  const MaxSum* ms = a.ms + (int64_t)r * a.n_seg;
+  const MaxSum* ms = a.ms + (int64_t)r * a.n_seg * kWaves;
   float tl = -INFINITY;
   const int x = td_token(a, r, t, tl);
   lx[t] = x;
   __syncthreads();
   bool first = x >= 0;   // the same token twice is one place of the row
-  for (int j = 0; j < t && first; ++j) first = lx[j] != x;
+  for (int j0 = 0; j0 < a.K; j0 += 8) {
+    int o[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) o[q] = lx[j0 + q];   // (-1 past the list)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) first = first && !(o[q] == x && j0 + q < t);
+  }
   const float l = x >= 0 ? logit_at<DT>(row_ptr<DT>(a.logits, a.ld, r), x) : -INFINITY;
   const int some = block_or(x >= 0 ? 1 : 0, redi);
 
   // the row: off the list relative to m_out, all of it relative to m
-  float m_out = -INFINITY;
-  for (int i = t; i < a.n_seg; i += kThreads) m_out = fmaxf(m_out, ms[i].m);
-  m_out = block_max(m_out, red);
-  double z_out = 0.0;
-  for (int i = t; i < a.n_seg; i += kThreads)
-    z_out += ms[i].m > -INFINITY ? (double)ms[i].s * (double)__builtin_amdgcn_exp2f((ms[i].m - m_out) * a.c)
-                                 : (double)ms[i].s;
-  z_out = block_sum_d(z_out, redd);
+  float m_out;
+  const double z_out = tr_total(ms, a.n_seg * kWaves, a.c, m_out, red, redd);
   const float m = fmaxf(m_out, block_max(l, red));
   const double e_l = x >= 0 ? exp2_split(((double)l - (double)m) * (double)a.c) : 0.0;
   const double f_out = m_out > -INFINITY ? exp2_split(((double)m_out - (double)m) * (double)a.c) : 0.0;
@@ -205,49 +174,53 @@ __global__ __launch_bounds__(kThreads) void k_td_loss(DistillArgs a) {
     o.pad = 0;
     a.rows[r] = o;
   }
+  const bool twice = block_or(x >= 0 && !first ? 1 : 0, redi) != 0;   // (uniform)
   if (x >= 0) {
-    double ps = 0.0;
-    for (int j = 0; j < a.K; ++j) ps += lx[j] == x ? lp[j] : 0.0;
+    double ps = p;
+    if (twice) {
+      ps = 0.0;
+      for (int j = 0; j < a.K; ++j) ps += lx[j] == x ? lp[j] : 0.0;
+    }
     a.d_list[(int64_t)r * a.K + t] = (float)(scale * (mass * e_l / z - ps));
   }
 }
 
-template <int DT, bool VEC>
+template <int DT>
 __global__ __launch_bounds__(kThreads) void k_td_grad(DistillArgs a) {
-  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * kTrSeg;
-  void* out = const_cast<void*>(row_ptr<DT>(a.d_logits, a.d_ld, r));
+  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * a.seg, n = min(a.seg, a.V - base);
+  constexpr int kSz = 16 / TrEl<DT>::n;   // bytes of a logit
+  void* out = (char*)const_cast<void*>(row_ptr<DT>(a.d_logits, a.d_ld, r)) + (int64_t)base * kSz;
   const DistillRow row = a.rows[r];
   float v[kTdPer];
   if (row.zero) {
 #pragma unroll
     for (int j = 0; j < kTdPer; ++j) v[j] = 0.f;
-    td_store<DT, VEC>(out, a.V, base, v);
+    td_store<DT>(out, n, v);
     return;
   }
-  td_load<DT, VEC>(row_ptr<DT>(a.logits, a.ld, r), a.V, base, v);
+  tr_load<DT>((const char*)row_ptr<DT>(a.logits, a.ld, r) + (int64_t)base * kSz, n, v);
 #pragma unroll
   for (int j = 0; j < kTdPer; ++j) v[j] = __builtin_amdgcn_exp2f((v[j] - row.m) * a.c) * row.f;
-  td_store<DT, VEC>(out, a.V, base, v);
+  td_store<DT>(out, n, v);
   wait_vmem();       // the list's tokens are written over what this stored
   __syncthreads();
   float tl;
-  const int x = td_token(a, r, threadIdx.x, tl);
-  if (x >= base && x < base + kTrSeg) td_put<DT>(out, x, a.d_list[(int64_t)r * a.K + threadIdx.x]);
+  const int x = td_token(a, r, threadIdx.x, tl) - base;
+  if (x >= 0 && x < a.seg) td_put<DT>(out, x, a.d_list[(int64_t)r * a.K + threadIdx.x]);
 }
 
 namespace {
-template <int DT, bool VEC>
+template <int DT>
 void topk_distill(const DistillArgs& a, hipStream_t st) {
   const dim3 segs((unsigned)(a.R * a.n_seg)), block(kThreads);
-  hipLaunchKernelGGL((k_td_stats<DT, VEC>), segs, block, 0, st, a);
+  hipLaunchKernelGGL((k_td_stats<DT>), segs, block, 0, st, a);
   hipLaunchKernelGGL((k_td_loss<DT>), dim3((unsigned)a.R), block, 0, st, a);
-  if (a.d_logits) hipLaunchKernelGGL((k_td_grad<DT, VEC>), segs, block, 0, st, a);
+  if (a.d_logits) hipLaunchKernelGGL((k_td_grad<DT>), segs, block, 0, st, a);
 }
 }  // namespace
 
-hipError_t launch_topk_distill(const DistillArgs& a, int dt, int vec, hipStream_t st) {
-  if (dt == kDtBF16) vec ? topk_distill<kDtBF16, true>(a, st) : topk_distill<kDtBF16, false>(a, st);
-  else vec ? topk_distill<kDtF32, true>(a, st) : topk_distill<kDtF32, false>(a, st);
+hipError_t launch_topk_distill(const DistillArgs& a, int dt, hipStream_t st) {
+  dt == kDtBF16 ? topk_distill<kDtBF16>(a, st) : topk_distill<kDtF32>(a, st);
   return hipGetLastError();
 }
 

@@ -1,21 +1,26 @@
 // spec_topk.hip -- the k largest logits of each row, with the row's log Z.
 //
-//   k_tk_seg    one workgroup per 8192 logits of a row, all in registers: the segment's maximum
-//               and sum of exponentials, and every logit that can be among the row's k largest
+//   k_tk_seg    one workgroup per segment of a row (up to 8192 logits, the row's segments equally
+//               long), all in registers, read once: each wave's maximum and sum of exponentials,
+//               and every logit that can be among the row's k largest
 //   k_tk_merge  one workgroup per row: the segments' candidates -> the k largest, in order
 //
-// A logit's 64-bit key holds its order key (a larger logit, a larger key; -0 counts as +0) above
-// the complement of its index, so that keys are distinct and equal logits rank by index.  The
-// k-th largest of a segment's 256 per-thread maxima (of each thread's two largest for k > 128) is
-// no larger than the segment's k-th largest logit, so what reaches it holds the segment's k
-// largest; for a row without order that is a few more than k.  Where more than `cap` reach it
-// (ties, an ordered row) the exact k-th key is found by bisection over its bits.
+// A candidate's 64-bit key holds its order key (a larger logit, a larger key; -0 counts as +0)
+// above the complement of its index, so that keys are distinct and equal logits rank by index.
+// What reaches a bound that at least k of a segment's per-thread maxima reach holds the segment's
+// k largest logits, and for a row without order few more.  Each wave finds the ceil(k / 4)-th
+// largest of its 64 maxima (of each thread's two largest for k > 128) to 16 bits by ballots; the
+// smallest of the four is such a bound, with no exchange but one.  (The exact k-th of the 256
+// maxima, by counting, made the kernel 140 us on 512 rows of 151,936.)  Where more than `cap`
+// logits reach it (ties, an ordered row) the k-th largest of one wave's maxima is tried, then the
+// exact k-th key is found by bisection.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "spec_device.h"
 #include "spec_train.h"
+#include "spec_train_device.h"
 
 namespace specv {
 
@@ -30,54 +35,11 @@ __device__ __forceinline__ float tk_value(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // tk_key(-inf)
 
-// Index of register j of this thread: 16-byte vectors dealt round-robin over the threads.
+// Index within the segment of register j of this thread (tr_load's order).
 template <int DT>
 __device__ __forceinline__ int tk_index(int j) {
-  constexpr int kEl = DT == kDtBF16 ? 8 : 4;
+  constexpr int kEl = TrEl<DT>::n;
   return kEl * ((int)threadIdx.x + kThreads * (j / kEl)) + j % kEl;
-}
-template <int DT, bool VEC>
-__device__ __forceinline__ void tk_load(const void* row, int V, int base, float (&v)[kPer]) {
-  constexpr int kEl = DT == kDtBF16 ? 8 : 4;
-#pragma unroll
-  for (int q = 0; q < kPer / kEl; ++q) {
-    const int e0 = base + tk_index<DT>(q * kEl);
-    if (VEC && e0 + kEl <= V) {
-      const uint4 x = ld_nt16((const char*)row + (int64_t)e0 * (16 / kEl));
-      if constexpr (DT == kDtBF16) {
-        v[8 * q + 0] = bf16_lo(x.x); v[8 * q + 1] = bf16_hi(x.x); v[8 * q + 2] = bf16_lo(x.y); v[8 * q + 3] = bf16_hi(x.y);
-        v[8 * q + 4] = bf16_lo(x.z); v[8 * q + 5] = bf16_hi(x.z); v[8 * q + 6] = bf16_lo(x.w); v[8 * q + 7] = bf16_hi(x.w);
-      } else {
-        v[4 * q + 0] = __uint_as_float(x.x); v[4 * q + 1] = __uint_as_float(x.y);
-        v[4 * q + 2] = __uint_as_float(x.z); v[4 * q + 3] = __uint_as_float(x.w);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kEl; ++e) v[kEl * q + e] = e0 + e < V ? logit_at<DT>(row, e0 + e) : -INFINITY;
-    }
-  }
-}
-
-// The K-th largest of the workgroup's 256 (NM = 1) or 512 (NM = 2) values x, by counting the
-// larger ones (ties by place); 1 <= K <= 256.
-template <typename T, int NM>
-__device__ __forceinline__ T kth_of_maxima(const T (&x)[NM], int K, T* lds, T* res) {
-#pragma unroll
-  for (int n = 0; n < NM; ++n) lds[NM * threadIdx.x + n] = x[n];
-  __syncthreads();
-  int rank[NM];
-#pragma unroll
-  for (int n = 0; n < NM; ++n) rank[n] = 0;
-  for (int i = 0; i < NM * kThreads; ++i) {
-    const T o = lds[i];
-#pragma unroll
-    for (int n = 0; n < NM; ++n) rank[n] += o > x[n] || (o == x[n] && i < (int)(NM * threadIdx.x + n)) ? 1 : 0;
-  }
-#pragma unroll
-  for (int n = 0; n < NM; ++n)
-    if (rank[n] == K - 1) *res = x[n];
-  __syncthreads();
-  return *res;
 }
 __device__ __forceinline__ int block_sum_i(int v, int* red) {
   v = wave_sum_i(v);
@@ -89,119 +51,207 @@ __device__ __forceinline__ int block_sum_i(int v, int* red) {
   __syncthreads();
   return r;
 }
+// The sum of the waves' values v (each uniform in its wave).
+__device__ __forceinline__ int block_add(int v, int* red) {
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  int r = red[0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) r += red[i];
+  __syncthreads();
+  return r;
+}
+// The kk-th largest of a wave's 64 NM 16-bit keys (0: there are not so many).
+template <int NM>
+__device__ __forceinline__ uint32_t wave_kth(const uint32_t (&key)[NM], int kk) {
+  uint32_t prefix = 0;
+#pragma unroll
+  for (int b = 15; b >= 0; --b) {
+    const uint32_t c = prefix | (1u << b);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NM; ++i) n += __popcll(__ballot(key[i] >= c));
+    prefix = n >= kk ? c : prefix;
+  }
+  return prefix;
+}
 
-template <int DT, bool VEC, int NM>
+template <int DT, int NM>
 __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
-  __shared__ uint32_t mx[NM * kThreads];
-  __shared__ uint32_t res;
+  __shared__ uint32_t wb[2][kWaves];
   __shared__ int red[2 * kWaves];
-  __shared__ int count;
   __shared__ float redf[2 * kWaves];
-  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * kTrSeg;
-  const void* row = row_ptr<DT>(a.logits, a.ld, r);
+  __shared__ int count;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * a.seg;
+  const int n_el = min(a.seg, a.V - base);
   float v[kPer];
-  tk_load<DT, VEC>(row, a.V, base, v);
+  tr_load<DT>((const char*)row_ptr<DT>(a.logits, a.ld, r) + (int64_t)base * (16 / TrEl<DT>::n), n_el, v);
   if (threadIdx.x == 0) count = 0;
   float m1 = -INFINITY, m2 = -INFINITY;
-  int bad = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    bad |= !(v[j] < INFINITY) ? 1 : 0;
     if constexpr (NM == 2) m2 = fmaxf(m2, fminf(m1, v[j]));
     m1 = fmaxf(m1, v[j]);
   }
-  const float m = block_max(m1, redf);
-  float s = 0.f;
-  if (m > -INFINITY) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) s += __builtin_amdgcn_exp2f((v[j] - m) * a.c);
-  }
-  bad = block_or(bad, red);
-  s = wave_sum(s);
-  if ((threadIdx.x & 63) == 0) redf[threadIdx.x >> 6] = s;
+  const float m = wave_max(m1);
+  const float s = wave_sum(tr_sum_exp(v, m, a.c));
   const int64_t slot = (int64_t)r * a.n_seg + seg;
-  if (bad) {   // uniform
-    if (threadIdx.x == 0) a.n_cand[slot] = -1;
-    return;
-  }
-  uint32_t x[NM];
-  x[0] = tk_key(m1);
-  if constexpr (NM == 2) x[1] = tk_key(m2);
-  uint32_t thr = kth_of_maxima<uint32_t, NM>(x, a.K, mx, &res);
-  if (threadIdx.x == 0) a.ms[slot] = MaxSum{m, (redf[0] + redf[1]) + (redf[2] + redf[3])};
-  if (thr <= kKeyNegInf) thr = kKeyNegInf + 1;   // a logit of -inf is no candidate
+  if (lane == 0) a.ms[slot * kWaves + wave] = MaxSum{m, s};
+  uint32_t key[NM];
+  key[0] = tk_key(m1) >> 16;
+  if constexpr (NM == 2) key[1] = tk_key(m2) >> 16;
+  uint32_t b = wave_kth<NM>(key, (a.K + kWaves - 1) / kWaves);
+  if (lane == 0) wb[0][wave] = b;
+  __syncthreads();
+  b = min(min(wb[0][0], wb[0][1]), min(wb[0][2], wb[0][3]));
+  // logits of -inf are no candidates; the bound's 16 bits stand for the least key that has them
+  float thr = tk_value(b << 16);
+  if (!(thr >= -0x1.fffffep127f)) thr = -0x1.fffffep127f;
   int n = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) n += tk_key(v[j]) >= thr ? 1 : 0;
-  const int total = block_sum_i(n, red);
-  int last = INT_MAX;   // of the keys equal to thr, those up to this index
-  if (total > a.cap) {
-    // exactly the K largest: the K-th largest key, then the index of its last one
-    uint32_t lo = thr, hi = 0xffffffffu;   // count(>= lo) >= K
-    while (lo < hi) {
-      const uint32_t mid = lo + (uint32_t)(((uint64_t)hi - lo + 1) / 2);
-      n = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) n += tk_key(v[j]) >= mid ? 1 : 0;
-      if (block_sum_i(n, red) >= a.K) lo = mid;
-      else hi = mid - 1;
-    }
-    thr = lo;
+  for (int j = 0; j < kPer; ++j) n += __popcll(__ballot(v[j] >= thr));
+  if (lane == 0) red[wave] = n;
+  __syncthreads();
+  int total = red[0] + red[1] + red[2] + red[3];
+  uint64_t* out = a.cand + slot * a.cap;
+  if (total > a.cap) {   // uniform
+    b = wave_kth<NM>(key, a.K);
+    if (lane == 0) wb[1][wave] = b;
+    const float mb = block_max(m1, redf);
+    b = max(max(wb[1][0], wb[1][1]), max(wb[1][2], wb[1][3]));
+    // keys of bf16 logits differ in their upper halves only
+    constexpr int kSh = DT == kDtBF16 ? 16 : 0;
+    uint32_t lo = max(tk_key(thr), b << 16), hi = tk_key(mb);   // at least K keys are >= lo
+    int last = INT_MAX;   // of the keys equal to lo, those up to this index
     n = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) n += tk_key(v[j]) > thr ? 1 : 0;
-    const int ties = a.K - block_sum_i(n, red);   // >= 1
-    int il = 0, ih = kTrSeg - 1;
-    while (il < ih) {
-      const int mid = (il + ih) / 2;
+    for (int j = 0; j < kPer; ++j) n += __popcll(__ballot(tk_key(v[j]) >= lo));
+    total = block_add(n, red);
+    // a bound that K to `cap` keys reach, or the K-th largest key itself
+    while (total > a.cap && lo >> kSh < hi >> kSh) {
+      const uint32_t mid = ((lo >> kSh) + ((hi >> kSh) - (lo >> kSh) + 1) / 2) << kSh;
       n = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) n += tk_key(v[j]) == thr && tk_index<DT>(j) <= mid ? 1 : 0;
-      if (block_sum_i(n, red) >= ties) ih = mid;
-      else il = mid + 1;
+      for (int j = 0; j < kPer; ++j) n += __popcll(__ballot(tk_key(v[j]) >= mid));
+      n = block_add(n, red);
+      if (n >= a.K) {
+        lo = mid;
+        total = n;
+      } else {
+        hi = mid - 1;
+      }
     }
-    last = il;
+    if (total > a.cap) {   // more equal logits than fit: the first of them by index
+      n = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) n += __popcll(__ballot((tk_key(v[j]) >> kSh) > (lo >> kSh)));
+      const int ties = a.K - block_add(n, red);   // >= 1
+      int il = 0, ih = kTrSeg - 1;
+      while (il < ih) {
+        const int mid = (il + ih) / 2;
+        n = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          n += __popcll(__ballot((tk_key(v[j]) >> kSh) == (lo >> kSh) && tk_index<DT>(j) <= mid));
+        if (block_add(n, red) >= ties) ih = mid;
+        else il = mid + 1;
+      }
+      last = il;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t k = tk_key(v[j]);
+      // (a NaN's key may pass: its row is not listed, but the list must not overflow)
+      if ((k >> kSh) > (lo >> kSh) || ((k >> kSh) == (lo >> kSh) && tk_index<DT>(j) <= last)) {
+        const int i = atomicAdd(&count, 1);
+        if (i < a.cap) out[i] = ((uint64_t)k << 32) | (uint32_t)~(base + tk_index<DT>(j));
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) a.n_cand[slot] = min(count, a.cap);
+    return;
   }
-  uint64_t* out = a.cand + slot * a.cap;
+  int at = 0;   // this wave's place in the list
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) at += w < wave ? red[w] : 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const uint32_t k = tk_key(v[j]);
-    if (k > thr || (k == thr && tk_index<DT>(j) <= last)) {
-      const int i = atomicAdd(&count, 1);
-      out[i] = ((uint64_t)k << 32) | (uint32_t)~(base + tk_index<DT>(j));
+    const uint64_t mask = __ballot(v[j] >= thr);
+    if (mask) {   // uniform in the wave
+      if (v[j] >= thr) {
+        const int i = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        out[i] = ((uint64_t)tk_key(v[j]) << 32) | (uint32_t)~(base + tk_index<DT>(j));
+      }
+      at += __popcll(mask);
     }
   }
-  __syncthreads();
-  if (threadIdx.x == 0) a.n_cand[slot] = count;
+  if (threadIdx.x == 0) a.n_cand[slot] = total;
 }
 
 constexpr int kMergeCap = 1024;   // candidates that are ranked against each other
+constexpr int kRankStep = 16;
+
+// f(key) for each of this thread's candidates (0 for none), eight loads at a time.  The segments'
+// lists are dealt out as one, candidate i to thread i mod 256: off[] holds where each list begins
+// in it, off[n_seg] their total.
+template <typename F>
+__device__ __forceinline__ void each_candidate(const TopkArgs& a, const uint64_t* cand, const int* off, F f) {
+  const int total = off[a.n_seg];
+  for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < total; i0 += 8 * kThreads) {
+    int at[8], seg[8];
+    uint64_t k[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      at[q] = min(i0 + q * kThreads, total - 1);
+      seg[q] = 0;
+    }
+    for (int b = a.seg_bit; b > 0; b >>= 1)   // the last list that begins at or before it
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int s = min(seg[q] + b, a.n_seg - 1);
+        seg[q] = off[s] <= at[q] ? s : seg[q];
+      }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) k[q] = cand[(int64_t)seg[q] * a.cap + at[q] - off[seg[q]]];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f(i0 + q * kThreads < total ? k[q] : 0);
+  }
+}
 
 template <int NM>
 __global__ __launch_bounds__(kThreads) void k_tk_merge(TopkArgs a) {
-  __shared__ uint64_t key[kMergeCap];
-  __shared__ uint64_t res;
+  __shared__ alignas(16) uint64_t key[kMergeCap + kRankStep];
+  __shared__ int off[kThreads + 1];
+  __shared__ uint32_t wb[kWaves];
   __shared__ int red[2 * kWaves];
   __shared__ float redf[2 * kWaves];
   __shared__ double redd[kWaves];
   __shared__ int count;
   const int r = blockIdx.x, t = threadIdx.x;
-  const MaxSum* ms = a.ms + (int64_t)r * a.n_seg;
-  const int32_t* nc = a.n_cand + (int64_t)r * a.n_seg;
+  const MaxSum* ms = a.ms + (int64_t)r * a.n_seg * kWaves;
   const uint64_t* cand = a.cand + (int64_t)r * a.n_seg * a.cap;
   int32_t* oi = a.index + (int64_t)r * a.K;
   float* ol = a.logit + (int64_t)r * a.K;
   const float nan = __int_as_float(0x7fc00000);
   if (t == 0) count = 0;
-  int bad = 0;
-  float m = -INFINITY;
-  for (int i = t; i < a.n_seg; i += kThreads) {
-    if (nc[i] < 0) bad = 1;
-    else m = fmaxf(m, ms[i].m);
+  static_assert(kTrMaxV / kTrSeg <= kThreads, "a thread for every segment");
+  // the lists' places, by a sum over the lanes and the waves before
+  const int nc = t < a.n_seg ? a.n_cand[(int64_t)r * a.n_seg + t] : 0;
+  int upto = nc;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(upto, d);
+    upto += (t & 63) >= d ? o : 0;
   }
-  bad = block_or(bad, red);
-  m = block_max(m, redf);
-  if (bad || m == -INFINITY) {   // NaN or +inf, or no finite logit
+  if ((t & 63) == 63) red[t >> 6] = upto;
+  __syncthreads();
+  for (int w = 0; w < (t >> 6); ++w) upto += red[w];
+  if (t <= a.n_seg) off[t] = upto - nc;      // (its total, for t = n_seg)
+  if (t == kThreads - 1) off[kThreads] = upto;
+  float m;
+  const double lz = tr_log_z(ms, a.n_seg * kWaves, a.c, a.inv_t, m, redf, redd);   // (orders off, count)
+  if (lz != lz) {   // NaN or +inf, or no finite logit: uniform
     for (int j = t; j < a.K; j += kThreads) {
       oi[j] = -1;
       ol[j] = nan;
@@ -209,57 +259,62 @@ __global__ __launch_bounds__(kThreads) void k_tk_merge(TopkArgs a) {
     if (t == 0 && a.log_z) a.log_z[r] = nan;
     return;
   }
-  double z = 0.0;
-  for (int i = t; i < a.n_seg; i += kThreads)
-    if (ms[i].m > -INFINITY) z += (double)ms[i].s * (double)__builtin_amdgcn_exp2f((ms[i].m - m) * a.c);
-  z = block_sum_d(z, redd);
-  if (t == 0 && a.log_z) a.log_z[r] = (float)((double)m * a.inv_t + log2_split(z) * 0.6931471805599453);
+  if (t == 0 && a.log_z) a.log_z[r] = (float)lz;
+  const int total = off[a.n_seg];
 
-  // the largest candidates of each thread, and from them a bound that the K largest reach
-  uint64_t x[NM];
-#pragma unroll
-  for (int n = 0; n < NM; ++n) x[n] = 0;
-  int total = 0;
-  const int n_all = a.n_seg * a.cap;
-  for (int i = t; i < n_all; i += kThreads)
-    if (i % a.cap < nc[i / a.cap]) {
-      const uint64_t k = cand[i];
-      ++total;
-      if constexpr (NM == 2) {
-        if (k > x[0]) { x[1] = x[0]; x[0] = k; }
-        else if (k > x[1]) x[1] = k;
-      } else {
-        x[0] = k > x[0] ? k : x[0];
-      }
-    }
-  total = block_sum_i(total, red);
+  // a bound that the K largest reach, as in a segment; each wave answers for its share
   uint64_t thr = 1;
-  if (total > kMergeCap) {
-    thr = kth_of_maxima<uint64_t, NM>(x, a.K, key, &res);
-    if (thr == 0) thr = 1;
-    int n = 0;
-    for (int i = t; i < n_all; i += kThreads) n += i % a.cap < nc[i / a.cap] && cand[i] >= thr ? 1 : 0;
-    if (block_sum_i(n, red) > kMergeCap) {
-      uint64_t lo = thr, hi = ~0ull;   // count(>= lo) >= K: the keys are distinct
-      while (lo < hi) {
-        const uint64_t mid = lo + (hi - lo) / 2 + 1;
-        n = 0;
-        for (int i = t; i < n_all; i += kThreads) n += i % a.cap < nc[i / a.cap] && cand[i] >= mid ? 1 : 0;
-        if (block_sum_i(n, red) >= a.K) lo = mid;
-        else hi = mid - 1;
-      }
-      thr = lo;
-    }
+  if (total > 2 * a.K + 64) {
+    uint32_t x[NM];
+#pragma unroll
+    for (int n = 0; n < NM; ++n) x[n] = 0;
+    int own = 0;
+    each_candidate(a, cand, off, [&](uint64_t k) {
+      const uint32_t h = (uint32_t)(k >> 48);
+      own += k != 0 ? 1 : 0;
+      if constexpr (NM == 2) x[1] = max(x[1], min(x[0], h));
+      x[0] = max(x[0], h);
+    });
+    own = wave_sum_i(own);
+    const int kk = (int)(((int64_t)a.K * own + total - 1) / total);
+    const uint32_t b = kk > 0 ? wave_kth<NM>(x, kk) : 0xffffu;
+    if ((t & 63) == 0) wb[t >> 6] = b;
     __syncthreads();
+    thr = (uint64_t)min(min(wb[0], wb[1]), min(wb[2], wb[3])) << 48;
+    if (thr == 0) thr = 1;
+    if (total > kMergeCap) {
+      int n = 0;
+      each_candidate(a, cand, off, [&](uint64_t k) { n += k >= thr ? 1 : 0; });
+      if (block_sum_i(n, red) > kMergeCap) {
+        uint64_t lo = thr, hi = ~0ull;   // at least K are >= lo, and the keys are distinct
+        while (lo < hi) {
+          const uint64_t mid = lo + (hi - lo) / 2 + 1;
+          n = 0;
+          each_candidate(a, cand, off, [&](uint64_t k) { n += k >= mid ? 1 : 0; });
+          if (block_sum_i(n, red) >= a.K) lo = mid;
+          else hi = mid - 1;
+        }
+        thr = lo;
+      }
+    }
   }
-  for (int i = t; i < n_all; i += kThreads)
-    if (i % a.cap < nc[i / a.cap] && cand[i] >= thr) key[atomicAdd(&count, 1)] = cand[i];
+  each_candidate(a, cand, off, [&](uint64_t k) {
+    if (k >= thr) key[atomicAdd(&count, 1)] = k;
+  });
   __syncthreads();
   const int n = count;
+  if (t < kRankStep) key[n + t] = 0;
+  __syncthreads();
   for (int i = t; i < n; i += kThreads) {
     const uint64_t k = key[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += key[j] > k ? 1 : 0;
+    for (int j = 0; j < n; j += kRankStep) {   // the reads of a step go out together
+      uint64_t o[kRankStep];
+#pragma unroll
+      for (int q = 0; q < kRankStep; ++q) o[q] = key[j + q];
+#pragma unroll
+      for (int q = 0; q < kRankStep; ++q) rank += o[q] > k ? 1 : 0;
+    }
     if (rank < a.K) {
       oi[rank] = (int32_t)~(uint32_t)k;
       ol[rank] = tk_value((uint32_t)(k >> 32));
@@ -272,21 +327,16 @@ __global__ __launch_bounds__(kThreads) void k_tk_merge(TopkArgs a) {
 }
 
 namespace {
-template <int DT, bool VEC, int NM>
+template <int DT, int NM>
 void row_topk(const TopkArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_tk_seg<DT, VEC, NM>), dim3((unsigned)(a.R * a.n_seg)), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((k_tk_seg<DT, NM>), dim3((unsigned)(a.R * a.n_seg)), dim3(kThreads), 0, st, a);
   hipLaunchKernelGGL((k_tk_merge<NM>), dim3((unsigned)a.R), dim3(kThreads), 0, st, a);
-}
-template <int DT, bool VEC>
-void row_topk_k(const TopkArgs& a, hipStream_t st) {
-  if (a.K > 128) row_topk<DT, VEC, 2>(a, st);
-  else row_topk<DT, VEC, 1>(a, st);
 }
 }  // namespace
 
-hipError_t launch_row_topk(const TopkArgs& a, int dt, int vec, hipStream_t st) {
-  if (dt == kDtBF16) vec ? row_topk_k<kDtBF16, true>(a, st) : row_topk_k<kDtBF16, false>(a, st);
-  else vec ? row_topk_k<kDtF32, true>(a, st) : row_topk_k<kDtF32, false>(a, st);
+hipError_t launch_row_topk(const TopkArgs& a, int dt, hipStream_t st) {
+  if (dt == kDtBF16) a.K > 128 ? row_topk<kDtBF16, 2>(a, st) : row_topk<kDtBF16, 1>(a, st);
+  else a.K > 128 ? row_topk<kDtF32, 2>(a, st) : row_topk<kDtF32, 1>(a, st);
   return hipGetLastError();
 }
 

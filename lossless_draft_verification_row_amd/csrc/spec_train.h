@@ -59,7 +59,7 @@ hipError_t launch_head_zero(uint16_t* d_weight, int64_t ld, int V, int D, hipStr
 
 // ---------------------------------------------------------------- top logits, distillation
 
-constexpr int kTrSeg = 8192;      // logits of one workgroup (32 per thread)
+constexpr int kTrSeg = 8192;      // most logits of one workgroup (32 per thread)
 constexpr int kTrMaxK = 256;      // longest list
 constexpr int kTrMaxV = 1 << 21;  // largest vocabulary
 
@@ -71,21 +71,27 @@ struct TopkArgs {
   const void* logits;             // [R, V], row stride ld
   int64_t ld;
   int R, V, K, n_seg, cap;
+  int seg;                        // logits of a segment
+  int seg_bit;                    // the largest power of two below n_seg (0 for one segment)
   float c;                        // log2(e) / T
   double inv_t;
   int32_t* index;                 // [R, K]
   float* logit;                   // [R, K]
   float* log_z;                   // [R] or nullptr
   uint64_t* cand;                 // [R][n_seg][cap]: order key and complemented index
-  int32_t* n_cand;                // [R][n_seg]; -1: the segment holds a NaN or +inf
-  MaxSum* ms;                     // [R][n_seg]
+  int32_t* n_cand;                // [R][n_seg]
+  MaxSum* ms;                     // [R][n_seg][4 waves]
 };
-// Candidates that a segment may hand on: its K largest always fit.
-inline int topk_cap(int K) { return (K + K / 2 + 32 + 15) & ~15; }
-hipError_t launch_row_topk(const TopkArgs& a, int dt, int vec, hipStream_t st);
+// Candidates that a segment may hand on, a power of two: its K largest always fit, and more
+// than twice as many unless K is near 256 (a row without order hands on about 1.5 K).
+inline int topk_cap(int K) { return K <= 16 ? 64 : K <= 48 ? 128 : K <= 112 ? 256 : 512; }
+// A row's segments: as few as hold it, equally long but for whole 16-byte vectors.
+inline int tr_n_seg(int V) { return (V + kTrSeg - 1) / kTrSeg; }
+inline int tr_seg(int V) { return ((V + tr_n_seg(V) - 1) / tr_n_seg(V) + 7) & ~7; }
+hipError_t launch_row_topk(const TopkArgs& a, int dt, hipStream_t st);
 
 struct DistillRow {               // what the gradient needs of a row
-  float m, f;                     // d = 2^((l - m) c) f outside the list
+  float m, f;                     // d = 2^((l - m) c) f off the list
   int zero;                       // the row's gradient is zero
   int pad;
 };
@@ -93,6 +99,7 @@ struct DistillArgs {
   const void* logits;             // [R, V] student rows, row stride ld
   int64_t ld;
   int R, V, K, n_seg;
+  int seg;                        // logits of a segment
   float c;                        // log2(e) / T
   double inv_t;
   const int32_t* index;           // [R, K] teacher's tokens
@@ -103,10 +110,10 @@ struct DistillArgs {
   float* log_z;                   // [R] or nullptr
   void* d_logits;                 // [R, V], row stride d_ld, of the logits' type, or nullptr; may be `logits`
   int64_t d_ld;
-  MaxSum* ms;                     // [R][n_seg]: the logits outside the list
+  MaxSum* ms;                     // [R][n_seg][4 waves]: the logits off the list
   DistillRow* rows;               // [R]
   float* d_list;                  // [R][K]: the gradient at the list's tokens
 };
-hipError_t launch_topk_distill(const DistillArgs& a, int dt, int vec, hipStream_t st);
+hipError_t launch_topk_distill(const DistillArgs& a, int dt, hipStream_t st);
 
 }  // namespace specv

@@ -28,7 +28,6 @@ struct Carve {
   }
 };
 
-int elem_bytes(spec_dtype dt) { return dt == SPEC_BF16 ? 2 : 4; }
 // A C caller's enum may hold any int, which is looked at as such.
 bool dtype_valid(const spec_dtype& dt) {
   int v;
@@ -39,7 +38,6 @@ bool dtype_valid(const spec_dtype& dt) {
 bool rows16(const void* p, int64_t ld, int elem) { return ((uintptr_t)p % 16) == 0 && (ld * elem) % 16 == 0; }
 bool temperature_valid(float t) { return t > 0.f && isfinite(t) && isfinite(1.f / t); }
 float exp2_scale(float t) { return (float)(1.4426950408889634 / (double)t); }
-int n_segments(int V) { return (V + kTrSeg - 1) / kTrSeg; }
 
 HlPlan hl_plan(int R, int V, int D) {
   HlPlan p;
@@ -64,10 +62,10 @@ void carve_topk(Carve& cv, TopkArgs& a) {
   const size_t n = (size_t)a.R * a.n_seg;
   a.cand = cv.take<uint64_t>(n * a.cap * sizeof(uint64_t));
   a.n_cand = cv.take<int32_t>(n * sizeof(int32_t));
-  a.ms = cv.take<MaxSum>(n * sizeof(MaxSum));
+  a.ms = cv.take<MaxSum>(n * kWaves * sizeof(MaxSum));
 }
 void carve_distill(Carve& cv, DistillArgs& a, bool grad) {
-  a.ms = cv.take<MaxSum>((size_t)a.R * a.n_seg * sizeof(MaxSum));
+  a.ms = cv.take<MaxSum>((size_t)a.R * a.n_seg * kWaves * sizeof(MaxSum));
   if (!grad) return;
   a.rows = cv.take<DistillRow>((size_t)a.R * sizeof(DistillRow));
   a.d_list = cv.take<float>((size_t)a.R * a.K * sizeof(float));
@@ -101,7 +99,7 @@ size_t spec_row_topk_workspace_bytes(int R, int V, int K) {
   TopkArgs a;
   memset(&a, 0, sizeof(a));
   a.R = R;
-  a.n_seg = n_segments(V);
+  a.n_seg = tr_n_seg(V);
   a.cap = topk_cap(K);
   Carve cv{nullptr};
   carve_topk(cv, a);
@@ -115,7 +113,7 @@ int spec_row_topk(int R, int V, int K, spec_dtype dt, const void* logits, int64_
   if (V > kTrMaxV || K > kTrMaxK || R > kMaxRows) return SPEC_ERR_UNSUPPORTED;
   if (R == 0) return SPEC_OK;
   if (!logits || ld < V || !out_index || !out_logit) return SPEC_ERR_INVALID;
-  if ((int64_t)R * n_segments(V) > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  if ((int64_t)R * tr_n_seg(V) > INT_MAX) return SPEC_ERR_UNSUPPORTED;
   const int ws = check_workspace(workspace, workspace_bytes, spec_row_topk_workspace_bytes(R, V, K));
   if (ws != SPEC_OK) return ws;
   TopkArgs a;
@@ -125,7 +123,9 @@ int spec_row_topk(int R, int V, int K, spec_dtype dt, const void* logits, int64_
   a.R = R;
   a.V = V;
   a.K = K;
-  a.n_seg = n_segments(V);
+  a.n_seg = tr_n_seg(V);
+  a.seg = tr_seg(V);
+  for (a.seg_bit = 0; (a.seg_bit ? 2 * a.seg_bit : 1) < a.n_seg;) a.seg_bit = a.seg_bit ? 2 * a.seg_bit : 1;
   a.cap = topk_cap(K);
   a.c = exp2_scale(temperature);
   a.inv_t = 1.0 / (double)temperature;
@@ -134,8 +134,7 @@ int spec_row_topk(int R, int V, int K, spec_dtype dt, const void* logits, int64_
   a.log_z = out_log_z;
   Carve cv{(char*)workspace};
   carve_topk(cv, a);
-  const hipError_t e = launch_row_topk(a, dt == SPEC_BF16 ? kDtBF16 : kDtF32, rows16(logits, ld, elem_bytes(dt)) ? 1 : 0,
-                                       (hipStream_t)hip_stream);
+  const hipError_t e = launch_row_topk(a, dt == SPEC_BF16 ? kDtBF16 : kDtF32, (hipStream_t)hip_stream);
   return e == hipSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
@@ -145,7 +144,7 @@ size_t spec_topk_distill_workspace_bytes(int R, int V, int K, int grad) {
   memset(&a, 0, sizeof(a));
   a.R = R;
   a.K = K;
-  a.n_seg = n_segments(V);
+  a.n_seg = tr_n_seg(V);
   Carve cv{nullptr};
   carve_distill(cv, a, grad != 0);
   return cv.off;
@@ -162,7 +161,7 @@ int spec_topk_distill(int R, int V, int K, spec_dtype dt, const void* logits, in
   if (d_logits && d_ld < V) return SPEC_ERR_INVALID;
   // in place: every logit and its gradient share their place, so the rows must too
   if (d_logits == logits && d_ld != ld) return SPEC_ERR_INVALID;
-  if ((int64_t)R * n_segments(V) > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  if ((int64_t)R * tr_n_seg(V) > INT_MAX) return SPEC_ERR_UNSUPPORTED;
   const int ws = check_workspace(workspace, workspace_bytes, spec_topk_distill_workspace_bytes(R, V, K, d_logits != nullptr));
   if (ws != SPEC_OK) return ws;
   DistillArgs a;
@@ -172,7 +171,8 @@ int spec_topk_distill(int R, int V, int K, spec_dtype dt, const void* logits, in
   a.R = R;
   a.V = V;
   a.K = K;
-  a.n_seg = n_segments(V);
+  a.n_seg = tr_n_seg(V);
+  a.seg = tr_seg(V);
   a.c = exp2_scale(temperature);
   a.inv_t = 1.0 / (double)temperature;
   a.index = index;
@@ -185,9 +185,7 @@ int spec_topk_distill(int R, int V, int K, spec_dtype dt, const void* logits, in
   a.d_ld = d_ld;
   Carve cv{(char*)workspace};
   carve_distill(cv, a, d_logits != nullptr);
-  const int es = elem_bytes(dt);
-  const int vec = rows16(logits, ld, es) && (!d_logits || rows16(d_logits, d_ld, es)) ? 1 : 0;
-  const hipError_t e = launch_topk_distill(a, dt == SPEC_BF16 ? kDtBF16 : kDtF32, vec, (hipStream_t)hip_stream);
+  const hipError_t e = launch_topk_distill(a, dt == SPEC_BF16 ? kDtBF16 : kDtF32, (hipStream_t)hip_stream);
   return e == hipSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 

@@ -8,6 +8,7 @@
 #include <stdlib.h>
 
 #include "host_stubs.h"
+#include "spec_device.h"
 #include "spec_train.h"
 #include "spec_verify.h"
 
@@ -15,18 +16,18 @@ using hoststub::carved;
 
 namespace specv {
 
-hipError_t launch_row_topk(const TopkArgs& a, int, int, hipStream_t) {
+hipError_t launch_row_topk(const TopkArgs& a, int, hipStream_t) {
   ++hoststub::g_launches;
   const size_t n = (size_t)a.R * a.n_seg;
   carved("candidates", a.cand, n * a.cap * sizeof(uint64_t));
   carved("candidate counts", a.n_cand, n * sizeof(int32_t));
-  carved("segment sums", a.ms, n * sizeof(MaxSum));
-  if (a.cap < a.K || (int64_t)a.n_seg * kTrSeg < a.V) ++hoststub::g_errors;
+  carved("segment sums", a.ms, n * kWaves * sizeof(MaxSum));
+  if (a.cap < a.K || (a.cap & (a.cap - 1)) || a.seg > kTrSeg || a.seg % 8 || (int64_t)a.n_seg * a.seg < a.V) ++hoststub::g_errors;
   return hipSuccess;
 }
-hipError_t launch_topk_distill(const DistillArgs& a, int, int, hipStream_t) {
+hipError_t launch_topk_distill(const DistillArgs& a, int, hipStream_t) {
   ++hoststub::g_launches;
-  carved("segment sums", a.ms, (size_t)a.R * a.n_seg * sizeof(MaxSum));
+  carved("segment sums", a.ms, (size_t)a.R * a.n_seg * kWaves * sizeof(MaxSum));
   if (a.d_logits) {
     carved("row factors", a.rows, (size_t)a.R * sizeof(DistillRow));
     carved("list gradients", a.d_list, (size_t)a.R * a.K * sizeof(float));
