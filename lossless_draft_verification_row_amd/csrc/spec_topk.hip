@@ -108,10 +108,18 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
   // logits of -inf are no candidates; the bound's 16 bits stand for the least key that has them
   float thr = tk_value(b << 16);
   if (!(thr >= -0x1.fffffep127f)) thr = -0x1.fffffep127f;
+  // each thread's candidates, and their places by a sum over the lanes
   int n = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) n += __popcll(__ballot(v[j] >= thr));
-  if (lane == 0) red[wave] = n;
+  for (int j = 0; j < kPer; ++j) n += v[j] >= thr ? 1 : 0;
+  int at = n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(at, d);
+    at += lane >= d ? o : 0;
+  }
+  if (lane == 63) red[wave] = at;
+  at -= n;
   __syncthreads();
   int total = red[0] + red[1] + red[2] + red[3];
   uint64_t* out = a.cand + slot * a.cap;
@@ -124,6 +132,7 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
     constexpr int kSh = DT == kDtBF16 ? 16 : 0;
     uint32_t lo = max(tk_key(thr), b << 16), hi = tk_key(mb);   // at least K keys are >= lo
     int last = INT_MAX;   // of the keys equal to lo, those up to this index
+    __syncthreads();
     n = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) n += __popcll(__ballot(tk_key(v[j]) >= lo));
@@ -172,20 +181,12 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
     if (threadIdx.x == 0) a.n_cand[slot] = min(count, a.cap);
     return;
   }
-  int at = 0;   // this wave's place in the list
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) at += w < wave ? red[w] : 0;
+  out += at;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const uint64_t mask = __ballot(v[j] >= thr);
-    if (mask) {   // uniform in the wave
-      if (v[j] >= thr) {
-        const int i = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-        out[i] = ((uint64_t)tk_key(v[j]) << 32) | (uint32_t)~(base + tk_index<DT>(j));
-      }
-      at += __popcll(mask);
-    }
-  }
+  for (int j = 0; j < kPer; ++j)
+    if (v[j] >= thr) *out++ = ((uint64_t)tk_key(v[j]) << 32) | (uint32_t)~(base + tk_index<DT>(j));
   if (threadIdx.x == 0) a.n_cand[slot] = total;
 }
 
