@@ -8,6 +8,7 @@ HIP kernels: there is no Python or CPU fallback, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -442,45 +443,57 @@ class _Call:
     that device's current one, made current inside (so that what the call allocates belongs to
     the stream its kernels run on)."""
 
+    __slots__ = ("device", "stream", "_ctx")
+
     def __init__(self, t, stream):
         if not t.is_cuda:
             raise ValueError("tensors must live on the GPU")
         self.device = t.device
-        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
-        if self.stream.device != t.device:
-            raise ValueError("the stream belongs to another device than the tensors")
-        self._ctx = torch.cuda.stream(self.stream)
+        if stream is None:
+            self.stream = torch.cuda.current_stream(self.device)
+            # the stream is its device's current one: only another device has to be made current
+            self._ctx = None if self.device.index == torch.cuda.current_device() else torch.cuda.device(self.device)
+        else:
+            if stream.device != t.device:
+                raise ValueError("the stream belongs to another device than the tensors")
+            self.stream = stream
+            self._ctx = torch.cuda.stream(stream)   # also makes the stream's device the current one
 
     def __enter__(self):
-        self._ctx.__enter__()   # also makes the stream's device the current one
+        if self._ctx is not None:
+            self._ctx.__enter__()
         return self
 
     def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
 
     def arg(self, t, name, dtype, shape, optional=False):
         """A contiguous tensor of this device, type and shape."""
         if t is None and optional:
             return None
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        if t.dtype != dtype or t.device != self.device or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
         return t.data_ptr()
 
     def rows(self, t, name, dtype, shape):
         """A 2-D tensor with unit column stride: its address and row stride."""
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != tuple(shape):
+        if t.dtype != dtype or t.device != self.device or t.shape != shape:
             raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {self.device}")
-        if shape[1] > 1 and t.stride(1) != 1:
+        ld, unit = t.stride()
+        if shape[1] > 1 and unit != 1:
             raise ValueError(f"{name} must have unit column stride")
-        if shape[0] > 1 and t.stride(0) < shape[1]:
+        if shape[0] > 1 and ld < shape[1]:
             raise ValueError(f"the rows of {name} overlap")
-        return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+        return t.data_ptr(), ld if shape[0] > 1 else max(shape[1], 1)
 
     def out(self, o, name, dtype, shape):
         """The caller's output tensor, or a new one."""
-        if o.get(name) is None:
-            o[name] = torch.empty(shape, dtype=dtype, device=self.device)
-        return self.arg(o[name], name, dtype, shape)
+        t = o.get(name)
+        if t is None:
+            t = o[name] = torch.empty(shape, dtype=dtype, device=self.device)
+            return t.data_ptr()
+        return self.arg(t, name, dtype, shape)
 
     def workspace(self, nbytes, workspace):
         """The caller's workspace, or one kept per device and stream: calls on one stream are
@@ -505,14 +518,17 @@ class _Call:
         return ws, ws.numel()
 
 
+@functools.lru_cache(maxsize=256)
 def spec_row_topk_workspace_bytes(R, V, K) -> int:
     return int(load_library().spec_row_topk_workspace_bytes(R, V, K))
 
 
+@functools.lru_cache(maxsize=256)
 def spec_topk_distill_workspace_bytes(R, V, K, grad) -> int:
     return int(load_library().spec_topk_distill_workspace_bytes(R, V, K, int(bool(grad))))
 
 
+@functools.lru_cache(maxsize=256)
 def spec_lm_head_loss_workspace_bytes(R, V, D, grad) -> int:
     return int(load_library().spec_lm_head_loss_workspace_bytes(R, V, D, int(bool(grad))))
 
@@ -535,7 +551,7 @@ def spec_row_topk(logits, k, *, temperature=1.0, workspace=None, out=None, strea
         o = out if out is not None else {}
         ptrs = (c.out(o, "index", torch.int32, (R, K)), c.out(o, "logit", torch.float32, (R, K)),
                 c.out(o, "log_z", torch.float32, (R,)))
-        ws, n = c.workspace(lib.spec_row_topk_workspace_bytes(R, V, K), workspace)
+        ws, n = c.workspace(spec_row_topk_workspace_bytes(R, V, K), workspace)
         rc = lib.spec_row_topk(R, V, K, dt, lp, ld, float(temperature), *ptrs, _ptr(ws), n, c.stream.cuda_stream)
     _check(rc, "spec_row_topk")
     return o
@@ -568,7 +584,7 @@ def spec_topk_distill(logits, index, teacher_logit, *, teacher_log_z=None, tempe
             if o.get("d_logits") is None:
                 o["d_logits"] = torch.empty((R, V), dtype=logits.dtype, device=c.device)
             dp, dld = c.rows(o["d_logits"], "d_logits", logits.dtype, (R, V))
-        ws, n = c.workspace(lib.spec_topk_distill_workspace_bytes(R, V, K, int(bool(grad))), workspace)
+        ws, n = c.workspace(spec_topk_distill_workspace_bytes(R, V, K, bool(grad)), workspace)
         rc = lib.spec_topk_distill(R, V, K, dt, lp, ld, xp, tp, zp, float(temperature), wp, loss, log_z, dp, dld,
                                    _ptr(ws), n, c.stream.cuda_stream)
     _check(rc, "spec_topk_distill")
@@ -604,7 +620,7 @@ def spec_lm_head_loss(hidden, weight, targets, *, temperature=1.0, row_weight=No
                 if o.get(key) is None:
                     o[key] = torch.empty((rows, D), dtype=bf16, device=c.device)
                 g[2 * i:2 * i + 2] = c.rows(o[key], key, bf16, (rows, D))
-        ws, n = c.workspace(lib.spec_lm_head_loss_workspace_bytes(R, V, D, int(bool(grad))), workspace)
+        ws, n = c.workspace(spec_lm_head_loss_workspace_bytes(R, V, D, bool(grad)), workspace)
         rc = lib.spec_lm_head_loss(R, V, D, hp, hld, wtp, wld, yp, float(temperature), wp, loss, log_z, *g, _ptr(ws), n,
                                    c.stream.cuda_stream)
     _check(rc, "spec_lm_head_loss")

@@ -4,16 +4,21 @@
 //   l_rv = sum_d h_rd W_vd,   loss_r = ln sum_v e^(l_rv / T) - l_(r, y_r) / T
 //   G_rv = w_r (softmax(l_r / T)_v - [v = y_r]) / T,   dh = G W,   dW = G^T h
 //
-// Forward: every 256-column tile of the logits leaves a maximum and a sum of exponentials per
-// row, which one small kernel folds.  Gradient: the vocabulary is taken in pieces; a piece's
+// Forward: every 256-column tile of the logits leaves a maximum and a sum of exponentials per row
+// and wave, which one small kernel folds.  Gradient: the vocabulary is taken in pieces; a piece's
 // logits are formed again, turned into G (bf16) and used at once in the two products, so that
 // the workspace holds G of one piece (at most 256 MB), never that of the whole vocabulary when
-// that is larger.  Work: 2RVD for the loss and 6RVD more for the gradient.
+// that is larger.  The last piece need not be formed again: the forward pass leaves its
+// exponentials, relative to their tile's maximum, where its G belongs, and one pass over them
+// makes them G when log Z is known.  Work: 2RVD for the loss, 4RVD for the products, and 2RVD for
+// the share of the vocabulary that lies in other pieces.
 //
-//   k_hl_prep     the target's logit, the row's scale, the hidden rows with those left out zeroed
-//   k_hl_stats    logit tiles -> (maximum, sum) per row and tile
+//   k_hl_stats    logit tiles -> (maximum, sum) per row and wave, exponentials of the last piece;
+//                 in further workgroups per row the target's logit, the row's scale and the hidden
+//                 row, zeroed if it is left out
 //   k_hl_rows     those -> log Z and the loss
-//   k_hl_grad     logit tiles -> G of one piece
+//   k_hl_scale    exponentials -> G of the last piece
+//   k_hl_grad     logit tiles -> G of another piece
 //   k_hl_dhidden  G W over a piece, fp32 parts kept per split of the piece
 //   k_hl_dweight  G^T h of a piece
 //   k_hl_reduce   the parts -> d_hidden
@@ -180,8 +185,11 @@ struct HlCore {
   static constexpr int kHold = 2;                                  // rows of step 1 before the barrier
   static constexpr int kRowLoads = (NA + NB + TI - 1) / TI;        // loads behind one row of MFMAs
   static constexpr int kReadRows = TI - kHold < 4 ? TI - kHold : 4;   // rows behind which B's reads go
-  static constexpr int kRowB = TJ / kReadRows;
-  static_assert(kRowB * kReadRows == TJ, "whole rows of B reads");
+  static constexpr int kRowB = (TJ + kReadRows - 1) / kReadRows;
+  static constexpr int b_reads(int row) {   // behind that row
+    const int left = TJ - kRowB * row;
+    return row < 0 || left < 0 ? 0 : left < kRowB ? left : kRowB;
+  }
 
   // One row of MFMAs with fragment reads (task 0 .. NT - 1) and loads (0 .. NL - 1) placed evenly
   // between them; each MFMA and what follows it is a scheduling region of its own.
@@ -208,7 +216,7 @@ struct HlCore {
                                                f32x4 (&acc)[TI][TJ]) {
     if constexpr (I < TI) {
       constexpr int n0 = (TI - kHold + I) * kRowLoads, n1 = n0 + kRowLoads < NA + NB ? n0 + kRowLoads : NA + NB;
-      constexpr int nl = I < kHold && n1 > n0 ? n1 - n0 : 0, nb = I < kReadRows ? kRowB : 0;
+      constexpr int nl = I < kHold && n1 > n0 ? n1 - n0 : 0, nb = b_reads(I);
       row<I, 1 + nb, nl>(
           fa, fb[0], acc,
           [&](int t) {
@@ -237,7 +245,7 @@ struct HlCore {
         __syncthreads();
       }
       constexpr int n0 = (I - kHold) * kRowLoads, n1 = n0 + kRowLoads < NA + NB ? n0 + kRowLoads : NA + NB;
-      constexpr int nl = I >= kHold && n1 > n0 ? n1 - n0 : 0, ib = I - kHold, nb = ib >= 0 && ib < kReadRows ? kRowB : 0;
+      constexpr int nl = I >= kHold && n1 > n0 ? n1 - n0 : 0, ib = I - kHold, nb = b_reads(ib);
       constexpr int na = I == 0 ? 1 : I == kHold ? kHold : I > kHold ? 1 : 0;
       row<I, na + nb, nl>(
           fa, fb[1], acc,
@@ -320,6 +328,12 @@ __device__ __forceinline__ int xcd_run(int n) {
   return x * (n >> 3) + min(x, n & 7) + (int)(blockIdx.x >> 3);
 }
 
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+constexpr float kKeepScale = 32768.f;   // kept exponentials are 2^15 e <= 2^15 in fp16
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const f16x2 v = {(_Float16)a, (_Float16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const bf16x2 v = {(__bf16)a, (__bf16)b};
   return __builtin_bit_cast(uint32_t, v);
@@ -353,8 +367,8 @@ __device__ __forceinline__ void store_rows(uint4* lds, int lane, int n_col, Put 
 // One wave per row (rows past R are set up as left out): the target's logit in fp32, the scale
 // of the row's gradient, and the hidden row with a row that is left out zeroed, so that what it
 // holds (padding may be NaN) never meets a product.
-__global__ __launch_bounds__(kThreads) void k_hl_prep(HlArgs a, int grad) {
-  const int lane = threadIdx.x & 63, r = blockIdx.x * kWaves + (threadIdx.x >> 6);
+__device__ __forceinline__ void prepare_row(const HlArgs& a, int block, int grad) {
+  const int lane = threadIdx.x & 63, r = block * kWaves + (threadIdx.x >> 6);
   if (r >= a.plan.Rp) return;
   int y = r < a.R ? a.targets[r] : -1;
   if (y >= a.V || y < 0) y = -1;
@@ -387,14 +401,21 @@ __global__ __launch_bounds__(kThreads) void k_hl_prep(HlArgs a, int grad) {
   }
 }
 
+// The first n_tiles workgroups take logit tiles, the others four rows each.  `keep` is the first
+// column of the piece whose exponentials are kept (V: none).
 template <int TI, int TJ, int WRN>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_stats(HlArgs a, int n_rt) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_stats(HlArgs a, int n_rt,
+                                                                                                 int n_tiles, int keep) {
   using Core = HlCore<TI, TJ, WRN, false, false>;
   __shared__ typename Core::Buf b0, b1;
+  if ((int)blockIdx.x >= n_tiles) {
+    prepare_row(a, blockIdx.x - n_tiles, a.d_weight != nullptr ? 1 : 0);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
   int rt, ct;
-  tile_of(xcd_run(gridDim.x), n_rt, a.plan.n_ct, rt, ct);
+  tile_of(xcd_run(n_tiles), n_rt, a.plan.n_ct, rt, ct);
   const int v0 = ct * kHlTile, r0 = rt * Core::BN;
   f32x4 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
@@ -402,10 +423,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
 
   // A lane holds 4 TI columns of TJ rows; the lanes 16, 32 and 48 on hold the rows' other columns
-  // of this wave, the other WRN - 1 waves those of the tile.  -inf keeps its weight 0; a NaN or
-  // +inf logit makes the sum NaN (inf - inf), also where it is all that a lane holds.
-  float2* part = (float2*)&b0;   // [WRN][BN]
-  const int vl = v0 + 16 * TI * wr + 4 * (lane >> 4);
+  // of this wave.  -inf keeps its weight 0; a NaN or +inf logit makes the sum NaN (inf - inf), also
+  // where it is all that a lane holds.
+  const int vw = 16 * TI * wr, vl = v0 + vw + 4 * (lane >> 4);
   if (v0 + kHlTile > a.V) {   // the vocabulary's last tile
 #pragma unroll
     for (int i = 0; i < TI; ++i)
@@ -429,64 +449,111 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * a.c);
+        for (int e = 0; e < 4; ++e) {
+          acc[i][j][e] = __builtin_amdgcn_exp2f((acc[i][j][e] - m) * a.c);
+          s += acc[i][j][e];
+        }
     } else {
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
           if (acc[i][j][e] != acc[i][j][e]) s = acc[i][j][e];
+          acc[i][j][e] = 0.f;
+        }
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (lane < 16) part[wr * Core::BN + 16 * (TJ * wc + j) + lane] = make_float2(m, s);
+    const int r = r0 + 16 * (TJ * wc + j) + lane;
+    if (lane < 16 && r < a.plan.Rp) a.rec[(int64_t)(ct * WRN + wr) * a.plan.Rp + r] = make_float2(m, s);
   }
-  __syncthreads();
-  for (int t = threadIdx.x; t < Core::BN; t += kThreads) {
-    const int r = r0 + t;
-    float m = -INFINITY, s = 0.f;
-#pragma unroll
-    for (int k = 0; k < WRN; ++k) m = fmaxf(m, part[k * Core::BN + t].x);
-#pragma unroll
-    for (int k = 0; k < WRN; ++k) {
-      const float2 p = part[k * Core::BN + t];
-      if (p.x > -INFINITY) s += p.y * __builtin_amdgcn_exp2f((p.x - m) * a.c);
-      else s += p.y;   // 0, or a NaN
-    }
-    if (r < a.plan.Rp) a.rec[(int64_t)ct * a.plan.Rp + r] = make_float2(m, s);
-  }
+  if (v0 < keep) return;   // uniform
+  const int n_vp = (a.V - keep + kHlDepth - 1) / kHlDepth * kHlDepth;
+  uint16_t* g0 = a.g + (int64_t)(r0 + 16 * TJ * wc) * a.plan.piece + (v0 - keep) + vw;
+  store_rows<TI, TJ>(
+      (wave & 2 ? b1.a : b0.a) + (wave & 1) * 32 * TI * TJ, lane, n_vp - (v0 - keep) - vw,
+      [&](int i, int j) {
+        // fp16 of 2^15 e: 11 bits down to 2^-29 of the wave's maximum, so that G's own rounding to
+        // bf16 is the only one that counts
+        return make_uint2(pack_f16(acc[i][j][0] * kKeepScale, acc[i][j][1] * kKeepScale),
+                          pack_f16(acc[i][j][2] * kKeepScale, acc[i][j][3] * kKeepScale));
+      },
+      [&](int r) { return r0 + 16 * TJ * wc + r < a.plan.Rp ? g0 + (int64_t)r * a.plan.piece : nullptr; });
 }
 
-// Sixteen rows per workgroup, sixteen threads to a row: the tiles' records in fp64.
-__global__ __launch_bounds__(kThreads) void k_hl_rows(HlArgs a) {
-  __shared__ float sm[16][17];
-  __shared__ double ss[16][17];
-  const int q = threadIdx.x >> 4, rl = threadIdx.x & 15;
-  const int r = blockIdx.x * 16 + rl;
+// Four rows per workgroup, 64 threads to a row: the waves' records, folded in fp64.
+__global__ __launch_bounds__(kThreads) void k_hl_rows(HlArgs a, int n_rec) {
+  __shared__ float sm[4][65];
+  __shared__ double ss[4][65];
+  constexpr int kQ = 64;
+  const int q = threadIdx.x >> 2, rl = threadIdx.x & 3;
+  const int r = blockIdx.x * 4 + rl, rc = min(r, a.R - 1);
   float m = -INFINITY;
-  if (r < a.R)
-    for (int k = q; k < a.plan.n_ct; k += 16) m = fmaxf(m, a.rec[(int64_t)k * a.plan.Rp + r].x);
-  sm[rl][q] = m;
-  __syncthreads();
+  double s = 0.0;   // relative to m; a record of maximum -inf holds 0 or a NaN
+  for (int k0 = q; k0 < n_rec; k0 += 4 * kQ) {
+    float2 p[4];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) m = fmaxf(m, sm[rl][k]);
-  double s = 0.0;
-  if (r < a.R)
-    for (int k = q; k < a.plan.n_ct; k += 16) {
-      const float2 p = a.rec[(int64_t)k * a.plan.Rp + r];
-      s += p.x > -INFINITY ? (double)p.y * (double)__builtin_amdgcn_exp2f((p.x - m) * a.c) : (double)p.y;
-    }
+    for (int u = 0; u < 4; ++u) p[u] = a.rec[(int64_t)min(k0 + kQ * u, n_rec - 1) * a.plan.Rp + rc];
+    float mx = m;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + kQ * u < n_rec) mx = fmaxf(mx, p[u].x);
+    if (m > -INFINITY) s *= exp2_split(((double)m - (double)mx) * (double)a.c);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + kQ * u < n_rec)
+        s += p[u].x > -INFINITY ? (double)p[u].y * (double)__builtin_amdgcn_exp2f((p[u].x - mx) * a.c) : (double)p[u].y;
+    m = mx;
+  }
+  sm[rl][q] = m;
   ss[rl][q] = s;
   __syncthreads();
   if (q != 0 || r >= a.R) return;
+  float mx = -INFINITY;
+  for (int k = 0; k < kQ; ++k) mx = fmaxf(mx, sm[rl][k]);
   double z = 0.0;
-  for (int k = 0; k < 16; ++k) z += ss[rl][k];
+  for (int k = 0; k < kQ; ++k)
+    z += sm[rl][k] > -INFINITY ? ss[rl][k] * exp2_split(((double)sm[rl][k] - (double)mx) * (double)a.c) : ss[rl][k];
   const double nan = __longlong_as_double(0x7ff8000000000000ll);
   const double l2 = z > 0.0 ? log2_split(z) : nan;
-  const double lz = (double)m * a.inv_t + l2 * 0.6931471805599453;
+  const double lz = (double)mx * a.inv_t + l2 * 0.6931471805599453;
   if (a.log_z) a.log_z[r] = (float)lz;
   if (a.loss) a.loss[r] = a.rows[r].y < 0 ? 0.f : (float)(lz - (double)a.ly[r] * a.inv_t);
-  a.rows[r].lz2 = (float)((double)m * (double)a.c + l2);
+  a.rows[r].lz2 = (float)((double)mx * (double)a.c + l2);
+}
+
+// Exponentials -> G of the last piece, in place, 32 bytes a thread: columns keep .. V - 1 and on
+// to the next multiple of 64 (whose exponentials are 0), rows 0 .. Rp - 1.  `cols` columns
+// share a record (one wave's of a tile).
+__global__ __launch_bounds__(kThreads) void k_hl_scale(HlArgs a, int keep, int cols, int n_chunk) {
+  const int r = blockIdx.x / n_chunk, v = ((blockIdx.x - r * n_chunk) * kThreads + (int)threadIdx.x) * 16;
+  const int n_vp = (a.V - keep + kHlDepth - 1) / kHlDepth * kHlDepth;
+  if (v >= n_vp) return;
+  const HlRow row = a.rows[r];
+  uint4* p = (uint4*)(a.g + (int64_t)r * a.plan.piece + v);
+  uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (row.scale != 0.f) {
+    const float m = a.rec[(int64_t)((keep + v) / cols) * a.plan.Rp + r].x;
+    // 2^-15 e^(m / T) / Z: nothing if the record's maximum is -inf (and NaN where Z is)
+    const float f = __builtin_amdgcn_exp2f(fmaf(m, a.c, -row.lz2)) * (1.f / kKeepScale);
+    const int y = row.y - keep - v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 x = p[h];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t g[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const f16x2 e = __builtin_bit_cast(f16x2, w[k]);
+        const float lo = (float)e[0] * f, hi = (float)e[1] * f;
+        const int at = 8 * h + 2 * k;
+        g[k] = pack_bf16((y == at ? lo - 1.f : lo) * row.scale, (y == at + 1 ? hi - 1.f : hi) * row.scale);
+      }
+      o[h] = make_uint4(g[0], g[1], g[2], g[3]);
+    }
+  }
+  p[0] = o[0];
+  p[1] = o[1];
 }
 
 // G of one piece: columns v0 .. v0 + n_v - 1 (n_v a multiple of 64 but for the vocabulary's end;
@@ -636,29 +703,38 @@ template <int TI, int TJ, int WRN>
 hipError_t head_loss(const HlArgs& a, hipStream_t st) {
   const HlPlan& p = a.plan;
   const bool grad = a.d_hidden || a.d_weight;
-  const int n_rt = (a.R + p.bn - 1) / p.bn, n_dt = (a.D + kHlTile - 1) / kHlTile;
-  hipLaunchKernelGGL(k_hl_prep, dim3((unsigned)((p.Rp + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a, grad ? 1 : 0);
-  hipLaunchKernelGGL((k_hl_stats<TI, TJ, WRN>), dim3((unsigned)(p.n_ct * n_rt)), dim3(kThreads), 0, st, a,
-                     n_rt);
-  hipLaunchKernelGGL(k_hl_rows, dim3((unsigned)((a.R + 15) / 16)), dim3(kThreads), 0, st, a);
+  const int n_rt = (a.R + p.bn - 1) / p.bn, n_rp = (p.Rp + p.bn - 1) / p.bn, n_dt = (a.D + kHlTile - 1) / kHlTile;
+  // the last piece's exponentials are kept by the first pass
+  const int keep = grad ? (p.n_ct * kHlTile - 1) / p.piece * p.piece : a.V;
+  const int n_tiles = p.n_ct * n_rt;
+  const dim3 block(kThreads);
+  hipLaunchKernelGGL((k_hl_stats<TI, TJ, WRN>), dim3((unsigned)(n_tiles + (p.Rp + kWaves - 1) / kWaves)), block, 0, st, a,
+                     n_rt, n_tiles, keep);
+  hipLaunchKernelGGL(k_hl_rows, dim3((unsigned)((a.R + 3) / 4)), block, 0, st, a, p.n_ct * WRN);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !grad) return e;
-  for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
+  // the pieces from the last one back, so that the one at hand comes first
+  bool first = true;
+  for (int64_t v0 = keep; v0 >= 0; v0 -= p.piece) {
     const int n_v = (int)(a.V - v0 < p.piece ? a.V - v0 : p.piece), n_ct = (n_v + kHlTile - 1) / kHlTile;
-    const int n_rp = (p.Rp + p.bn - 1) / p.bn;
-    hipLaunchKernelGGL((k_hl_grad<TI, TJ, WRN>), dim3((unsigned)(n_ct * n_rp)), dim3(kThreads), 0, st, a,
-                       (int)v0, n_v, n_rp);
+    if (first) {
+      const int n_chunk = (n_v + 16 * kThreads - 1) / (16 * kThreads);
+      hipLaunchKernelGGL(k_hl_scale, dim3((unsigned)(n_chunk * p.Rp)), block, 0, st, a, (int)v0, kHlTile / WRN, n_chunk);
+    } else {
+      hipLaunchKernelGGL((k_hl_grad<TI, TJ, WRN>), dim3((unsigned)(n_ct * n_rp)), block, 0, st, a, (int)v0, n_v, n_rp);
+    }
     if (a.d_hidden)
-      hipLaunchKernelGGL((k_hl_dhidden<TI, TJ, WRN>), dim3((unsigned)(n_dt * n_rt * p.n_split)), dim3(kThreads), 0, st,
-                         a, (int)v0, n_v, n_rt, n_dt, v0 > 0 ? 1 : 0);
+      hipLaunchKernelGGL((k_hl_dhidden<TI, TJ, WRN>), dim3((unsigned)(n_dt * n_rt * p.n_split)), block, 0, st, a, (int)v0,
+                         n_v, n_rt, n_dt, first ? 0 : 1);
     if (a.d_weight)
-      hipLaunchKernelGGL(k_hl_dweight, dim3((unsigned)(n_dt * n_ct)), dim3(kThreads), 0, st, a, (int)v0, n_v, n_dt);
+      hipLaunchKernelGGL(k_hl_dweight, dim3((unsigned)(n_dt * n_ct)), block, 0, st, a, (int)v0, n_v, n_dt);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
+    first = false;
   }
   if (a.d_hidden) {
     const int64_t n4 = (int64_t)a.R * (a.D / 4);
-    hipLaunchKernelGGL(k_hl_reduce, dim3((unsigned)((n4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL(k_hl_reduce, dim3((unsigned)((n4 + kThreads - 1) / kThreads)), block, 0, st, a);
   }
   return hipGetLastError();
 }
@@ -666,9 +742,14 @@ hipError_t head_loss(const HlArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_head_loss(const HlArgs& a, hipStream_t st) {
-  if (a.plan.bn == 64) return head_loss<4, 4, 4>(a, st);
-  if (a.plan.bn == 128) return head_loss<8, 4, 2>(a, st);
-  return head_loss<8, 8, 2>(a, st);
+  switch (a.plan.bn) {
+    case 64: return head_loss<4, 4, 4>(a, st);
+    case 128: return head_loss<8, 4, 2>(a, st);
+    case 160: return head_loss<8, 5, 2>(a, st);
+    case 192: return head_loss<8, 6, 2>(a, st);
+    case 224: return head_loss<8, 7, 2>(a, st);
+    default: return head_loss<8, 8, 2>(a, st);
+  }
 }
 
 }  // namespace specv

@@ -24,7 +24,8 @@ struct HlRow {                    // what the gradient tiles need of a row
 struct HlPlan {
   int Rp;                         // rows rounded up to whole stages (the gradient tiles' k)
   int n_ct;                       // vocabulary tiles
-  int bn;                         // rows per tile: 64, 128 or 256
+  int bn;                         // rows per tile: 64, 128, 160, 192, 224 or 256
+  int n_wave;                     // waves that share a row of a tile: 4 (bn 64) or 2
   int piece;                      // vocabulary columns whose logit gradients are held at a time
   int n_split;                    // parts of a piece's k in the product for the hidden states' gradient
 };
@@ -46,11 +47,12 @@ struct HlArgs {
   uint16_t* d_weight;             // [V, D] bf16, row stride dw_ld, or nullptr
   int64_t dw_ld;
   HlPlan plan;
-  float2* rec;                    // [n_ct][Rp]: a tile's maximum of a row and sum of 2^((l - m) c)
+  float2* rec;                    // [n_ct][n_wave][Rp]: a wave's maximum of a row and sum of 2^((l - m) c)
   float* ly;                      // [Rp]: the target's logit
   HlRow* rows;                    // [Rp]
   uint16_t* hz;                   // [Rp][D]: the hidden rows, those left out zeroed
-  uint16_t* g;                    // [Rp][piece]: dL/dl of the piece at hand, bf16
+  uint16_t* g;                    // [Rp][piece]: dL/dl of the piece at hand, bf16 (the last piece: first
+                                  // 2^15 2^((l - m) c), fp16)
   float* part;                    // [n_split][Rp][D]: parts of the hidden states' gradient
 };
 

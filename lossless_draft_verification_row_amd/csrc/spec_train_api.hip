@@ -43,7 +43,11 @@ HlPlan hl_plan(int R, int V, int D) {
   HlPlan p;
   p.Rp = (int)(((int64_t)R + kHlDepth - 1) / kHlDepth * kHlDepth);
   p.n_ct = (int)(((int64_t)V + kHlTile - 1) / kHlTile);
-  p.bn = R <= 64 ? 64 : R <= 128 ? 128 : 256;
+  // rows per tile: as few tiles of up to 256 rows as hold them, cut to the multiple of 32 that does
+  // (448 rows: two of 224, not two of 256, an eighth less work)
+  const int n_rt = (int)(((int64_t)R + 255) / 256);
+  p.bn = R <= 64 ? 64 : R <= 128 ? 128 : (int)(((int64_t)R + 32 * n_rt - 1) / (32 * n_rt) * 32);
+  p.n_wave = p.bn == 64 ? 4 : 2;
   // G of a piece within 256 MB (one tile's columns at least): the memory-side cache's size
   const int64_t cols = ((int64_t)1 << 27) / p.Rp / kHlTile * kHlTile;
   const int64_t all = (int64_t)p.n_ct * kHlTile;
@@ -72,7 +76,7 @@ void carve_distill(Carve& cv, DistillArgs& a, bool grad) {
 }
 void carve_head(Carve& cv, HlArgs& a, bool grad) {
   const HlPlan& p = a.plan;
-  a.rec = cv.take<float2>((size_t)p.n_ct * p.Rp * sizeof(float2));
+  a.rec = cv.take<float2>((size_t)p.n_ct * p.n_wave * p.Rp * sizeof(float2));
   a.ly = cv.take<float>((size_t)p.Rp * sizeof(float));
   a.rows = cv.take<HlRow>((size_t)p.Rp * sizeof(HlRow));
   if (!grad) return;
@@ -243,7 +247,8 @@ int spec_lm_head_loss(int R, int V, int D, const void* hidden, int64_t h_ld, con
   a.dw_ld = dw_ld;
   a.plan = hl_plan(R, V, D);
   const int64_t n_rt = ((int64_t)a.plan.Rp + a.plan.bn - 1) / a.plan.bn, n_dt = (D + kHlTile - 1) / kHlTile;
-  if ((a.plan.n_ct + 8) * (n_rt > n_dt ? n_rt : n_dt) > INT_MAX || n_rt * n_dt * a.plan.n_split > INT_MAX ||
+  if (a.plan.n_ct * (n_rt > n_dt ? n_rt : n_dt) > INT_MAX - kMaxRows || n_rt * n_dt * a.plan.n_split > INT_MAX ||
+      (int64_t)a.plan.Rp * (a.plan.piece / (16 * kThreads) + 1) > INT_MAX ||
       (int64_t)R * D / 4 > (int64_t)INT_MAX * kThreads || (int64_t)V * D / 8 > (int64_t)INT_MAX * kThreads)
     return SPEC_ERR_UNSUPPORTED;
   const bool grad = d_hidden || d_weight;

@@ -37,9 +37,10 @@ hipError_t launch_topk_distill(const DistillArgs& a, int, hipStream_t) {
 hipError_t launch_head_loss(const HlArgs& a, hipStream_t) {
   ++hoststub::g_launches;
   const HlPlan& p = a.plan;
-  carved("tile records", a.rec, (size_t)p.n_ct * p.Rp * sizeof(float2));
+  carved("tile records", a.rec, (size_t)p.n_ct * p.n_wave * p.Rp * sizeof(float2));
   carved("target logits", a.ly, (size_t)p.Rp * sizeof(float));
   carved("rows", a.rows, (size_t)p.Rp * sizeof(HlRow));
+  if (p.bn < 64 || p.bn > 256 || p.bn % 32 || (p.bn > 64 && p.bn < 128)) ++hoststub::g_errors;
   if (p.Rp < a.R || p.Rp % kHlDepth || p.piece % kHlTile || p.piece <= 0 || p.n_split < 1) ++hoststub::g_errors;
   // a piece's gradient stays within 256 MB, or one tile's columns
   if (p.piece > kHlTile && (int64_t)p.Rp * p.piece * 2 > ((int64_t)1 << 28)) ++hoststub::g_errors;
