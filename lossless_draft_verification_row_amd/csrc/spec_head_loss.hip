@@ -35,6 +35,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4), may_alias));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2), may_alias));
 typedef __attribute__((address_space(3))) void* lds_void_t;
 typedef __attribute__((address_space(3))) s16x4* lds_s4_t;
 
@@ -51,6 +53,7 @@ struct HlOperand {
 
 constexpr int kGran = kHlDepth / 8;    // 16-byte granules of a k-contiguous row per stage
 constexpr int kFarOffset = 0x7ffffff0;
+constexpr int kCus = 256;              // workgroups of a persistent kernel: one per CU
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage_rsrc(const HlOperand& o, int64_t skip, int64_t past) {
   const int64_t left = o.bytes - skip - past;
@@ -58,6 +61,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage_rsrc(const HlOperand& o,
   return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)o.p + skip), (short)0, n, 0x00020000);
 }
 
+// Wait for this wave's LDS accesses.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | 3 << 14 | 7 << 4); }
 // Wait until at most N of this wave's vector memory accesses are in flight.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -162,6 +167,10 @@ struct HlCore {
     asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+  // The first product of a tile: c = a b, so that nothing has to be cleared before.
+  static __device__ __forceinline__ void mma_first(f32x4& c, const bf16x8& a, const bf16x8& b) {
+    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
+  }
 
   struct Wave {
     int lane, wave;
@@ -170,7 +179,8 @@ struct HlCore {
     int oa[8], ob[8];
   };
   // Loads n0 .. n1 - 1 of stage s (A's, then B's); a stage past the last one has an empty resource,
-  // which loads nothing.
+  // which reads as zeros.  (No branch inside the loop: one makes the register allocator move
+  // accumulators and fragments about.)
   static __device__ __forceinline__ void loads(Buf& b, const HlOperand& A, const HlOperand& B, const Wave& w, int s,
                                                int n_k, int k_len, int n0, int n1) {
     const int64_t past = s < n_k ? 0 : (int64_t)1 << 62;
@@ -193,12 +203,13 @@ struct HlCore {
 
   // One row of MFMAs with fragment reads (task 0 .. NT - 1) and loads (0 .. NL - 1) placed evenly
   // between them; each MFMA and what follows it is a scheduling region of its own.
-  template <int I, int NT, int NL, typename Task, typename Load>
+  template <int I, int NT, int NL, bool FIRST, typename Task, typename Load>
   static __device__ __forceinline__ void row(const bf16x8 (&fa)[TI], const bf16x8 (&fb)[TJ], f32x4 (&acc)[TI][TJ],
                                              Task task, Load ld) {
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      mma(acc[I][j], fa[I], fb[j]);
+      if constexpr (FIRST) mma_first(acc[I][j], fa[I], fb[j]);
+      else mma(acc[I][j], fa[I], fb[j]);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         if (t * TJ / NT == j) task(t);
@@ -210,14 +221,15 @@ struct HlCore {
   }
   // Rows I .. of step 0: the previous row's A fragment and some of B's are read for step 1, and
   // the last of stage s + 1's loads go out.
-  template <int I>
+  // FIRST: of a tile's stage 0, whose stage 1 is loaded already.
+  template <int I, bool FIRST>
   static __device__ __forceinline__ void rows0(Buf& cur, Buf& next, const HlOperand& A, const HlOperand& B, const Wave& w,
                                                int s, int n_k, int k_len, bf16x8 (&fa)[TI], bf16x8 (&fb)[2][TJ],
                                                f32x4 (&acc)[TI][TJ]) {
     if constexpr (I < TI) {
       constexpr int n0 = (TI - kHold + I) * kRowLoads, n1 = n0 + kRowLoads < NA + NB ? n0 + kRowLoads : NA + NB;
-      constexpr int nl = I < kHold && n1 > n0 ? n1 - n0 : 0, nb = b_reads(I);
-      row<I, 1 + nb, nl>(
+      constexpr int nl = !FIRST && I < kHold && n1 > n0 ? n1 - n0 : 0, nb = b_reads(I);
+      row<I, 1 + nb, nl, FIRST>(
           fa, fb[0], acc,
           [&](int t) {
             if (t == 0) {
@@ -228,12 +240,12 @@ struct HlCore {
             }
           },
           [&](int l) { loads(next, A, B, w, s + 1, n_k, k_len, n0 + l, n0 + l + 1); });
-      rows0<I + 1>(cur, next, A, B, w, s, n_k, k_len, fa, fb, acc);
+      rows0<I + 1, FIRST>(cur, next, A, B, w, s, n_k, k_len, fa, fb, acc);
     }
   }
   // Rows I .. of step 1: from row kHold on the next stage's first fragments are read and this
   // buffer is loaded with stage s + 2.
-  template <int I>
+  template <int I, int SLACK>
   static __device__ __forceinline__ void rows1(Buf& cur, Buf& next, const HlOperand& A, const HlOperand& B, const Wave& w,
                                                int s, int n_k, int k_len, bf16x8 (&fa)[TI], bf16x8 (&fb)[2][TJ],
                                                f32x4 (&acc)[TI][TJ]) {
@@ -241,13 +253,15 @@ struct HlCore {
       if constexpr (I == kHold) {
         // this wave's loads of stage s + 1 have landed and its reads of stage s are done, and
         // after the barrier everyone's
-        wait_vmem();
-        __syncthreads();
+        if constexpr (SLACK > 0) wait_vm<SLACK>();
+        else wait_vmem();
+        wait_lds();
+        __builtin_amdgcn_s_barrier();
       }
       constexpr int n0 = (I - kHold) * kRowLoads, n1 = n0 + kRowLoads < NA + NB ? n0 + kRowLoads : NA + NB;
       constexpr int nl = I >= kHold && n1 > n0 ? n1 - n0 : 0, ib = I - kHold, nb = b_reads(ib);
       constexpr int na = I == 0 ? 1 : I == kHold ? kHold : I > kHold ? 1 : 0;
-      row<I, na + nb, nl>(
+      row<I, na + nb, nl, false>(
           fa, fb[1], acc,
           [&](int t) {
             if (t < na) {
@@ -259,35 +273,39 @@ struct HlCore {
             }
           },
           [&](int l) { loads(cur, A, B, w, s + 2, n_k, k_len, n0 + l, n0 + l + 1); });
-      rows1<I + 1>(cur, next, A, B, w, s, n_k, k_len, fa, fb, acc);
+      rows1<I + 1, SLACK>(cur, next, A, B, w, s, n_k, k_len, fa, fb, acc);
     }
   }
 
-  // n_k stages (an odd number is followed by one of zeros); k_len (of a k-contiguous operand)
-  // beyond which k reads as zero
-  static __device__ __forceinline__ void run(Buf& b0, Buf& b1, const HlOperand& A, const HlOperand& B, int n_k, int k_len,
-                                             f32x4 (&acc)[TI][TJ]) {
+  // The parts of a tile's address work that its place does not change.
+  static __device__ __forceinline__ Wave wave_of(int64_t lda, int64_t ldb) {
     Wave w;
     w.lane = threadIdx.x & 63;
     w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    w.sa = (KMA ? kHlDepth * A.ld : kHlDepth) * 2;
-    w.sb = (KMB ? kHlDepth * B.ld : kHlDepth) * 2;
+    w.sa = (KMA ? kHlDepth * lda : kHlDepth) * 2;
+    w.sb = (KMB ? kHlDepth * ldb : kHlDepth) * 2;
 #pragma unroll
-    for (int n = 0; n < NA; ++n) w.va[n] = load_offset<KMA, NA>(n, w.wave, w.lane, A.ld);
+    for (int n = 0; n < NA; ++n) w.va[n] = load_offset<KMA, NA>(n, w.wave, w.lane, lda);
 #pragma unroll
-    for (int n = 0; n < NB; ++n) w.vb[n] = load_offset<KMB, NB>(n, w.wave, w.lane, B.ld);
+    for (int n = 0; n < NB; ++n) w.vb[n] = load_offset<KMB, NB>(n, w.wave, w.lane, ldb);
     frag_offsets<KMA>(16 * TI * (w.wave / WCN), w.lane, w.oa);
     frag_offsets<KMB>(16 * TJ * (w.wave % WCN), w.lane, w.ob);
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-    constexpr int kFirst = (TI - kHold) * kRowLoads < NA + NB ? (TI - kHold) * kRowLoads : NA + NB;
+    return w;
+  }
+  // The loads of a tile's first two stages.
+  static __device__ __forceinline__ void begin(Buf& b0, Buf& b1, const HlOperand& A, const HlOperand& B, const Wave& w,
+                                               int n_k, int k_len) {
     loads(b0, A, B, w, 0, n_k, k_len, 0, NA + NB);
-    loads(b1, A, B, w, 1, n_k, k_len, 0, kFirst);
-    wait_vm<kFirst>();   // stage 0's loads
+    loads(b1, A, B, w, 1, n_k, k_len, 0, NA + NB);
+  }
+  // A tile whose begin() has been: n_k stages (an odd number is followed by one of zeros); k_len
+  // (of a k-contiguous operand) beyond which k reads as zero.  Where n_k is 0 the result is 0.  With
+  // STORES > 0 exactly so many stores of this wave lie behind begin()'s loads (or every load has
+  // landed): the first two stages' waits leave them in flight.  Loads and stores complete in their order.
+  template <int STORES = 0>
+  static __device__ __forceinline__ void run(Buf& b0, Buf& b1, const HlOperand& A, const HlOperand& B, const Wave& w,
+                                             int n_k, int k_len, f32x4 (&acc)[TI][TJ]) {
+    wait_vm<NA + NB + STORES>();   // stage 0's loads
     __builtin_amdgcn_s_barrier();
     bf16x8 fa[TI], fb[2][TJ];
 #pragma unroll
@@ -296,15 +314,26 @@ struct HlCore {
     for (int i = 0; i < TI - 1; ++i) fa[i] = frag<KMA>(b0.a, w.oa, i, 0);
     // two stages a turn, so that either buffer is known where it is read or loaded: the compiler
     // makes an LDS read wait for every load in flight into what it may alias
-    for (int s = 0; s < n_k; s += 2) {
-      rows0<0>(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
-      rows1<0>(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
-      rows0<0>(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
-      rows1<0>(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
+    rows0<0, true>(b0, b1, A, B, w, 0, n_k, k_len, fa, fb, acc);
+    rows1<0, STORES>(b0, b1, A, B, w, 0, n_k, k_len, fa, fb, acc);
+    rows0<0, false>(b1, b0, A, B, w, 1, n_k, k_len, fa, fb, acc);
+    rows1<0, 0>(b1, b0, A, B, w, 1, n_k, k_len, fa, fb, acc);
+    for (int s = 2; s < n_k; s += 2) {
+      rows0<0, false>(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
+      rows1<0, 0>(b0, b1, A, B, w, s, n_k, k_len, fa, fb, acc);
+      rows0<0, false>(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
+      rows1<0, 0>(b1, b0, A, B, w, s + 1, n_k, k_len, fa, fb, acc);
     }
     settle();
     wait_vmem();
-    __syncthreads();   // every wave is done with the stage buffers
+    wait_lds();
+    __builtin_amdgcn_s_barrier();   // every wave is done with the stage buffers
+  }
+  static __device__ __forceinline__ void run_one(Buf& b0, Buf& b1, const HlOperand& A, const HlOperand& B, int n_k,
+                                                 int k_len, f32x4 (&acc)[TI][TJ]) {
+    const Wave w = wave_of(A.ld, B.ld);
+    begin(b0, b1, A, B, w, n_k, k_len);
+    run(b0, b1, A, B, w, n_k, k_len, acc);
   }
 };
 
@@ -339,6 +368,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// What this wave has written to LDS before is read by its other lanes after: LDS serves a wave's
+// accesses in order, so that the compiler alone has to keep it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // A wave's 16 TI columns x 16 TJ rows as bf16 by way of LDS (16 TI bytes x 2 a row, the wave's own
 // 32 TI TJ 16 bytes), so that what it stores are whole rows' pieces of 32 TI bytes: the lanes' own
 // four columns of sixteen rows would be 32-byte pieces.  put(i, j) gives block (i, j)'s four packed
@@ -352,15 +388,15 @@ __device__ __forceinline__ void store_rows(uint4* lds, int lane, int n_col, Put 
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int r = 16 * j + (lane & 15), g = 2 * i + (lane >> 5);
-      ((uint2*)&lds[r * kG + (g ^ (r & (kG - 1)))])[(lane >> 4) & 1] = put(i, j);
+      ((u32x2*)&lds[r * kG + (g ^ (r & (kG - 1)))])[(lane >> 4) & 1] = put(i, j);
     }
-  __builtin_amdgcn_wave_barrier();
+  wave_sync();
 #pragma unroll
   for (int n = 0; n < TJ * 16 * kG / 64; ++n) {
     const int r = n * (64 / kG) + lane / kG, g = lane % kG;
     uint16_t* p = row(r);
-    const uint4 x = lds[r * kG + (g ^ (r & (kG - 1)))];
-    if (p && 8 * g < n_col) *(uint4*)(p + 8 * g) = x;
+    const u32x4 x = *(const u32x4*)&lds[r * kG + (g ^ (r & (kG - 1)))];
+    if (p && 8 * g < n_col) *(u32x4*)(p + 8 * g) = x;
   }
 }
 
@@ -420,7 +456,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   f32x4 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
   const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
-  Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
+  Core::run_one(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
 
   // A lane holds 4 TI columns of TJ rows; the lanes 16, 32 and 48 on hold the rows' other columns
   // of this wave.  -inf keeps its weight 0; a NaN or +inf logit makes the sum NaN (inf - inf), also
@@ -475,51 +511,61 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
       [&](int i, int j) {
         // fp16 of 2^15 e: 11 bits down to 2^-29 of the wave's maximum, so that G's own rounding to
         // bf16 is the only one that counts
-        return make_uint2(pack_f16(acc[i][j][0] * kKeepScale, acc[i][j][1] * kKeepScale),
-                          pack_f16(acc[i][j][2] * kKeepScale, acc[i][j][3] * kKeepScale));
+        return u32x2{pack_f16(acc[i][j][0] * kKeepScale, acc[i][j][1] * kKeepScale),
+                          pack_f16(acc[i][j][2] * kKeepScale, acc[i][j][3] * kKeepScale)};
       },
       [&](int r) { return r0 + 16 * TJ * wc + r < a.plan.Rp ? g0 + (int64_t)r * a.plan.piece : nullptr; });
 }
 
+// (m, s) takes in (mo, so): sums of 2^((l - m) c) relative to their maxima; one of maximum -inf is 0,
+// or a NaN.
+__device__ __forceinline__ void take_in(float& m, double& s, float mo, double so, float c) {
+  const float mx = fmaxf(m, mo);
+  if (m > -INFINITY) s *= (double)__builtin_amdgcn_exp2f((m - mx) * c);
+  if (mo > -INFINITY) so *= (double)__builtin_amdgcn_exp2f((mo - mx) * c);
+  s += so;
+  m = mx;
+}
+
 // Four rows per workgroup, 64 threads to a row: the waves' records, folded in fp64.
 __global__ __launch_bounds__(kThreads) void k_hl_rows(HlArgs a, int n_rec) {
-  __shared__ float sm[4][65];
-  __shared__ double ss[4][65];
-  constexpr int kQ = 64;
-  const int q = threadIdx.x >> 2, rl = threadIdx.x & 3;
+  __shared__ float sm[kWaves][4];
+  __shared__ double ss[kWaves][4];
+  const int q = threadIdx.x >> 2, rl = threadIdx.x & 3, wave = threadIdx.x >> 6;
   const int r = blockIdx.x * 4 + rl, rc = min(r, a.R - 1);
   float m = -INFINITY;
-  double s = 0.0;   // relative to m; a record of maximum -inf holds 0 or a NaN
-  for (int k0 = q; k0 < n_rec; k0 += 4 * kQ) {
-    float2 p[4];
+  double s = 0.0;
+  for (int k0 = q; k0 < n_rec; k0 += 8 * 64) {
+    float2 p[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) p[u] = a.rec[(int64_t)min(k0 + kQ * u, n_rec - 1) * a.plan.Rp + rc];
-    float mx = m;
+    for (int u = 0; u < 8; ++u) p[u] = a.rec[(int64_t)min(k0 + 64 * u, n_rec - 1) * a.plan.Rp + rc];
+    float mx = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (k0 + kQ * u < n_rec) mx = fmaxf(mx, p[u].x);
-    if (m > -INFINITY) s *= exp2_split(((double)m - (double)mx) * (double)a.c);
+    for (int u = 0; u < 8; ++u)
+      if (k0 + 64 * u < n_rec) mx = fmaxf(mx, p[u].x);
+    double t = 0.0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (k0 + kQ * u < n_rec)
-        s += p[u].x > -INFINITY ? (double)p[u].y * (double)__builtin_amdgcn_exp2f((p[u].x - mx) * a.c) : (double)p[u].y;
-    m = mx;
+    for (int u = 0; u < 8; ++u)
+      if (k0 + 64 * u < n_rec)
+        t += p[u].x > -INFINITY ? (double)p[u].y * (double)__builtin_amdgcn_exp2f((p[u].x - mx) * a.c) : (double)p[u].y;
+    take_in(m, s, mx, t, a.c);
   }
-  sm[rl][q] = m;
-  ss[rl][q] = s;
+#pragma unroll
+  for (int d = 4; d < 64; d <<= 1) take_in(m, s, __shfl_xor(m, d), __shfl_xor(s, d), a.c);
+  if ((threadIdx.x & 63) < 4) {
+    sm[wave][rl] = m;
+    ss[wave][rl] = s;
+  }
   __syncthreads();
-  if (q != 0 || r >= a.R) return;
-  float mx = -INFINITY;
-  for (int k = 0; k < kQ; ++k) mx = fmaxf(mx, sm[rl][k]);
-  double z = 0.0;
-  for (int k = 0; k < kQ; ++k)
-    z += sm[rl][k] > -INFINITY ? ss[rl][k] * exp2_split(((double)sm[rl][k] - (double)mx) * (double)a.c) : ss[rl][k];
+  if (threadIdx.x >= 4 || r >= a.R) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) take_in(m, s, sm[w][rl], ss[w][rl], a.c);
   const double nan = __longlong_as_double(0x7ff8000000000000ll);
-  const double l2 = z > 0.0 ? log2_split(z) : nan;
-  const double lz = (double)mx * a.inv_t + l2 * 0.6931471805599453;
+  const double l2 = s > 0.0 ? log2_split(s) : nan;
+  const double lz = (double)m * a.inv_t + l2 * 0.6931471805599453;
   if (a.log_z) a.log_z[r] = (float)lz;
   if (a.loss) a.loss[r] = a.rows[r].y < 0 ? 0.f : (float)(lz - (double)a.ly[r] * a.inv_t);
-  a.rows[r].lz2 = (float)((double)mx * (double)a.c + l2);
+  a.rows[r].lz2 = (float)((double)m * (double)a.c + l2);
 }
 
 // Exponentials -> G of the last piece, in place, 32 bytes a thread: columns keep .. V - 1 and on
@@ -571,7 +617,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   f32x4 acc[TI][TJ];
   const HlOperand A = {a.weight + (int64_t)v0 * a.w_ld, a.w_ld, extent(a.V, a.D, a.w_ld, v0, 0)};
   const HlOperand B = {a.hidden + (int64_t)r0 * a.h_ld, a.h_ld, extent(a.R, a.D, a.h_ld, r0, 0)};
-  Core::run(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
+  Core::run_one(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
   const int n_vp = (n_v + kHlDepth - 1) / kHlDepth * kHlDepth;
   const int vw = 16 * TI * wr;                        // the wave's first column within the tile
   float lz2[TJ], scale[TJ];
@@ -599,7 +645,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
         }
         // G is rounded to bf16 (half a step, 2^-9 of each entry): both products take bf16
         // operands, and the errors of a row's entries are independent
-        return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        return u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
       },
       [&](int r) { return r0 + 16 * TJ * wc + r < a.plan.Rp ? g0 + (int64_t)r * a.plan.piece : nullptr; });
 }
@@ -625,7 +671,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
                        extent(a.V, a.D, a.w_ld, pv0 + k0, d0)};
   const HlOperand B = {a.g + (int64_t)r0 * a.plan.piece + k0, a.plan.piece,
                        extent(a.plan.Rp, a.plan.piece, a.plan.piece, r0, k0)};
-  Core::run(b0, b1, A, B, s1 - s0, (s1 - s0) * kHlDepth, acc);
+  Core::run_one(b0, b1, A, B, s1 - s0, (s1 - s0) * kHlDepth, acc);
   float* part = a.part + (int64_t)sp * a.plan.Rp * a.D;
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
@@ -648,28 +694,79 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
 }
 
 // dW[v][d] of the piece: k = r, A = h (k major, rows d), B = G (k major, rows v).
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_hl_dweight(HlArgs a, int pv0,
-                                                                                                   int n_v, int n_dt) {
-  constexpr int TI = 8, TJ = 8, WRN = 2;
+//
+// With few rows a tile's product is short against what surrounds it (448 rows: 7 us of MFMAs, 15 us
+// of waiting for the first loads and of storing 128 KB), so each CU's workgroup goes through tiles
+// with the next one's first two stages on their way while this one's result leaves, through LDS of
+// its own, and does not wait for the stores before its third stage.
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_hl_dweight(
+    HlArgs a, int pv0, int n_v, int n_dt, int n_tiles) {
+  constexpr int TI = 8, TJ = 8, WRN = 2, kStores = 32;
   using Core = HlCore<TI, TJ, WRN, true, true>;
   __shared__ typename Core::Buf b0, b1;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ uint4 out[kWaves][32 * 2 * TI];   // 32 rows of a wave's 128 columns
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / Core::WCN, wc = wave % Core::WCN;
-  int dt, ct;
-  tile_of(xcd_run(gridDim.x), n_dt, (n_v + kHlTile - 1) / kHlTile, dt, ct);
-  const int d0 = dt * kHlTile, vt0 = ct * kHlTile;
+  const int n_ct = (n_v + kHlTile - 1) / kHlTile;
+  // this XCD's run of the tiles, and this workgroup's of them
+  const int x = blockIdx.x & 7, x0 = x * (n_tiles >> 3) + min(x, n_tiles & 7), nx = (n_tiles >> 3) + (x < (n_tiles & 7) ? 1 : 0);
+  const int step = ((int)gridDim.x - x + 7) >> 3;
+  const typename Core::Wave w = Core::wave_of(a.D, a.plan.piece);
+  const int n_k = a.plan.Rp / kHlDepth;
   f32x4 acc[TI][TJ];
-  const HlOperand A = {a.hz + d0, a.D, extent(a.plan.Rp, a.D, a.D, 0, d0)};
-  const HlOperand B = {a.g + vt0, a.plan.piece, extent(a.plan.Rp, a.plan.piece, a.plan.piece, 0, vt0)};
-  Core::run(b0, b1, A, B, a.plan.Rp / kHlDepth, a.plan.Rp, acc);
-  const int vw = vt0 + 16 * TJ * wc, dw = d0 + 16 * TI * wr;   // the wave's first row and column
-  uint16_t* o0 = a.d_weight + (int64_t)(pv0 + vw) * a.dw_ld + dw;
-  store_rows<TI, TJ>(
-      (wave & 2 ? b1.a : b0.a) + (wave & 1) * 32 * TI * TJ, lane, a.D - dw,
-      [&](int i, int j) {
-        return make_uint2(pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]));
-      },
-      [&](int r) { return vw + r < n_v ? o0 + r * a.dw_ld : nullptr; });
+  int i = blockIdx.x >> 3;
+  if (i >= nx) return;
+  int d0, vt0;
+  HlOperand A, B;
+  const auto place = [&](int u) {
+    int dt, ct;
+    tile_of(x0 + u, n_dt, n_ct, dt, ct);
+    d0 = dt * kHlTile;
+    vt0 = ct * kHlTile;
+    A = {a.hz + d0, a.D, extent(a.plan.Rp, a.D, a.D, 0, d0)};
+    B = {a.g + vt0, a.plan.piece, extent(a.plan.Rp, a.plan.piece, a.plan.piece, 0, vt0)};
+  };
+  place(i);
+  Core::begin(b0, b1, A, B, w, n_k, a.plan.Rp);
+  wait_vmem();
+  for (;;) {
+    Core::template run<kStores>(b0, b1, A, B, w, n_k, a.plan.Rp, acc);
+    const int vw = vt0 + 16 * TJ * wc, dw = d0 + 16 * TI * wr;   // this tile's, of the wave
+    i += step;
+    const bool more = i < nx;
+    if (more) {
+      place(i);
+      Core::begin(b0, b1, A, B, w, n_k, a.plan.Rp);
+    }
+    // kStores stores, whatever of them lies outside the matrix or the piece (their offsets do too)
+    const __amdgpu_buffer_rsrc_t rs =
+        stage_rsrc({a.d_weight + (int64_t)(pv0 + vw) * a.dw_ld + dw, a.dw_ld, extent(a.V, a.D, a.dw_ld, pv0 + vw, dw)}, 0, 0);
+    uint4* o = out[wave];
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));   // (the offsets below are formed here, not kept from tile to tile)
+#pragma unroll
+    for (int c = 0; c < TJ / 2; ++c) {
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+        for (int ii = 0; ii < TI; ++ii) {
+          const f32x4 v = acc[ii][2 * c + jj];
+          const int r = 16 * jj + (lane & 15), g = 2 * ii + (lane >> 5);
+          ((u32x2*)&o[r * 16 + (g ^ (r & 15))])[(lane >> 4) & 1] = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        }
+      wave_sync();
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int r = 4 * n + (lane >> 4), g = lane & 15, row = 32 * c + r;
+        const u32x4 v = *(const u32x4*)&o[r * 16 + (g ^ (r & 15))];
+        const bool in = vw + row < n_v && dw + 8 * g < a.D;
+        const int off = in ? (int)(row * a.dw_ld * 2) + 16 * g : kFarOffset;
+        __builtin_amdgcn_raw_buffer_store_b128(v, rs, off, 0, 0);
+      }
+      wave_sync();
+    }
+    if (!more) break;
+  }
 }
 
 // d_hidden = the splits' parts, added in order, rounded once.
@@ -727,7 +824,8 @@ hipError_t head_loss(const HlArgs& a, hipStream_t st) {
       hipLaunchKernelGGL((k_hl_dhidden<TI, TJ, WRN>), dim3((unsigned)(n_dt * n_rt * p.n_split)), block, 0, st, a, (int)v0,
                          n_v, n_rt, n_dt, first ? 0 : 1);
     if (a.d_weight)
-      hipLaunchKernelGGL(k_hl_dweight, dim3((unsigned)(n_dt * n_ct)), block, 0, st, a, (int)v0, n_v, n_dt);
+      hipLaunchKernelGGL(k_hl_dweight, dim3((unsigned)(n_dt * n_ct < kCus ? n_dt * n_ct : kCus)), block, 0, st, a, (int)v0,
+                         n_v, n_dt, n_dt * n_ct);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     first = false;

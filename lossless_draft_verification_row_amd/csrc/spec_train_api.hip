@@ -225,7 +225,7 @@ int spec_lm_head_loss(int R, int V, int D, const void* hidden, int64_t h_ld, con
   if (D % 8 != 0 || !rows16(hidden, h_ld, 2) || !rows16(weight, w_ld, 2)) return SPEC_ERR_UNSUPPORTED;
   if ((d_hidden && !rows16(d_hidden, dh_ld, 2)) || (d_weight && !rows16(d_weight, dw_ld, 2))) return SPEC_ERR_UNSUPPORTED;
   // a tile's rows are addressed with 32-bit byte offsets (256 rows x stride x 2 B < 2^31)
-  if (h_ld > kTrMaxV || w_ld > kTrMaxV) return SPEC_ERR_UNSUPPORTED;
+  if (h_ld > kTrMaxV || w_ld > kTrMaxV || dh_ld > kTrMaxV || dw_ld > kTrMaxV) return SPEC_ERR_UNSUPPORTED;
   HlArgs a;
   memset(&a, 0, sizeof(a));
   a.hidden = (const uint16_t*)hidden;
