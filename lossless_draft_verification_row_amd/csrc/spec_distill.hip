@@ -106,66 +106,109 @@ __global__ __launch_bounds__(kThreads) void k_td_stats(DistillArgs a) {
   if ((t & 63) == 0) a.ms[((int64_t)r * a.n_seg + seg) * kWaves + (t >> 6)] = MaxSum{m, s};
 }
 
+// One workgroup per row.  Its time is a chain of latencies, so everything it reads goes out first and
+// the reductions go in three rounds.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_td_loss(DistillArgs a) {
   __shared__ alignas(16) int lx[kTrMaxK];
   __shared__ double lp[kTrMaxK];
-  __shared__ float red[2 * kWaves];
-  __shared__ int redi[2 * kWaves];
-  __shared__ double redd[kWaves];
-  const int r = blockIdx.x, t = threadIdx.x;
+  __shared__ float rm[kWaves][3];
+  __shared__ int any[kWaves], twice[kWaves];
+  __shared__ double rs[kWaves][3], rt[kWaves];
+  const int r = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const MaxSum* ms = a.ms + (int64_t)r * a.n_seg * kWaves;
+  const int n_ms = a.n_seg * kWaves;
+  MaxSum part = {-INFINITY, 0.f};
+  if (t < n_ms) part = ms[t];
+  const float lz_t = a.teacher_log_z ? a.teacher_log_z[r] : 0.f;
+  const float weight = a.row_weight ? a.row_weight[r] : 1.f;
   float tl = -INFINITY;
   const int x = td_token(a, r, t, tl);
   lx[t] = x;
+  const float l = x >= 0 ? logit_at<DT>(row_ptr<DT>(a.logits, a.ld, r), x) : -INFINITY;
+
+  // maxima: off the list, on it, the teacher's
+  float m_out = part.m, m_in = l, tm = x >= 0 ? tl : -INFINITY;
+  for (int i = t + kThreads; i < n_ms; i += kThreads) m_out = fmaxf(m_out, ms[i].m);
+  m_out = wave_max(m_out);
+  m_in = wave_max(m_in);
+  tm = wave_max(tm);
+  const int any_w = __any(x >= 0) ? 1 : 0;
+  if (lane == 0) {
+    rm[wave][0] = m_out;
+    rm[wave][1] = m_in;
+    rm[wave][2] = tm;
+    any[wave] = any_w;
+  }
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    m_out = fmaxf(m_out, rm[w][0]);
+    m_in = fmaxf(m_in, rm[w][1]);
+    tm = fmaxf(tm, rm[w][2]);
+  }
+  const bool some = any[0] | any[1] | any[2] | any[3];
+  const float m = fmaxf(m_out, m_in);
   bool first = x >= 0;   // the same token twice is one place of the row
   for (int j0 = 0; j0 < a.K; j0 += 8) {
-    int o[8];
+    int e[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) o[q] = lx[j0 + q];   // (-1 past the list)
+    for (int q = 0; q < 8; ++q) e[q] = lx[j0 + q];   // (-1 past the list)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) first = first && !(o[q] == x && j0 + q < t);
+    for (int q = 0; q < 8; ++q) first = first && !(e[q] == x && j0 + q < t);
   }
-  const float l = x >= 0 ? logit_at<DT>(row_ptr<DT>(a.logits, a.ld, r), x) : -INFINITY;
-  const int some = block_or(x >= 0 ? 1 : 0, redi);
 
-  // the row: off the list relative to m_out, all of it relative to m
-  float m_out;
-  const double z_out = tr_total(ms, a.n_seg * kWaves, a.c, m_out, red, redd);
-  const float m = fmaxf(m_out, block_max(l, red));
+  // sums: off the list relative to m_out, on it relative to m, the teacher's masses
+  const auto term_of = [&](const MaxSum& p) {
+    return p.m > -INFINITY ? (double)p.s * exp2_split(((double)p.m - (double)m_out) * (double)a.c) : (double)p.s;
+  };
+  double z_out = t < n_ms ? term_of(part) : 0.0;
+  for (int i = t + kThreads; i < n_ms; i += kThreads) z_out += term_of(ms[i]);
   const double e_l = x >= 0 ? exp2_split(((double)l - (double)m) * (double)a.c) : 0.0;
+  const double at = x >= 0 ? (a.teacher_log_z ? (double)tl * a.inv_t - (double)lz_t : ((double)tl - (double)tm) * a.inv_t) : 0.0;
+  double p = x >= 0 ? exp(at) : 0.0;
+  double s_in = wave_sum_d(first ? e_l : 0.0), s_p = wave_sum_d(p);
+  z_out = wave_sum_d(z_out);
+  if (lane == 0) {
+    rs[wave][0] = z_out;
+    rs[wave][1] = s_in;
+    rs[wave][2] = s_p;
+  }
+  const int twice_w = __any(x >= 0 && !first) ? 1 : 0;
+  __syncthreads();
+  z_out = (rs[0][0] + rs[1][0]) + (rs[2][0] + rs[3][0]);
+  s_in = (rs[0][1] + rs[1][1]) + (rs[2][1] + rs[3][1]);
+  s_p = (rs[0][2] + rs[1][2]) + (rs[2][2] + rs[3][2]);
   const double f_out = m_out > -INFINITY ? exp2_split(((double)m_out - (double)m) * (double)a.c) : 0.0;
-  double z = block_sum_d(first ? e_l : 0.0, redd) + (m_out > -INFINITY ? z_out * f_out : z_out);
+  double z = s_in + (m_out > -INFINITY ? z_out * f_out : z_out);
   if (!(m > -INFINITY)) z = __longlong_as_double(0x7ff8000000000000ll);   // no finite logit
   const double lz = (double)m * a.inv_t + log(z);
-
-  // the teacher
-  double ln_p = -INFINITY, p = 0.0, rho = 0.0;
-  const float tm = block_max(x >= 0 ? tl : -INFINITY, red);
+  double ln_p = at, sum_p = s_p, rho = 0.0;
   if (a.teacher_log_z) {
-    if (x >= 0) ln_p = (double)tl * a.inv_t - (double)a.teacher_log_z[r];
-  } else {
-    const double zt = block_sum_d(x >= 0 ? exp(((double)tl - (double)tm) * a.inv_t) : 0.0, redd);
-    if (x >= 0) ln_p = ((double)tl - (double)tm) * a.inv_t - log(zt);
-  }
-  if (x >= 0) p = exp(ln_p);
-  lp[t] = p;
-  const double sum_p = block_sum_d(p, redd);
-  if (a.teacher_log_z) {
-    rho = 1.0 - sum_p;
+    rho = 1.0 - s_p;
     if (rho <= kTdTailMin) rho = 0.0;
+  } else if (some) {   // the list is the teacher
+    ln_p = at - log(s_p);
+    p /= s_p;
+    sum_p = s_p == s_p ? 1.0 : s_p;
   }
-  const double term = p > 0.0 ? p * (ln_p - ((double)l * a.inv_t - lz)) : p;   // p is 0, or NaN
-  double loss = block_sum_d(term, redd);
+  lp[t] = p;
+  double term = p > 0.0 ? p * (ln_p - ((double)l * a.inv_t - lz)) : p;   // p is 0, or NaN
+  term = wave_sum_d(term);
+  if (lane == 0) {
+    rt[wave] = term;
+    twice[wave] = twice_w;
+  }
+  __syncthreads();
+  double loss = (rt[0] + rt[1]) + (rt[2] + rt[3]);
   if (rho > 0.0) loss += rho * (log(rho) - (z_out > 0.0 ? (double)m_out * a.inv_t + log(z_out) - lz : -INFINITY));
   if (z != z) loss = z;
   if (t == 0) {
-    if (a.loss) a.loss[r] = some ? (float)loss : 0.f;
+    a.loss[r] = some ? (float)loss : 0.f;
     if (a.log_z) a.log_z[r] = (float)lz;
   }
   if (!a.d_logits) return;
-  const double scale = (a.row_weight ? (double)a.row_weight[r] : 1.0) * a.inv_t, mass = sum_p + rho;
+  const double scale = (double)weight * a.inv_t, mass = sum_p + rho;
   if (t == 0) {
     DistillRow o;
     o.m = m_out > -INFINITY ? m_out : 0.f;   // nothing off the list: its -inf logits give 0, not NaN
@@ -174,10 +217,9 @@ __global__ __launch_bounds__(kThreads) void k_td_loss(DistillArgs a) {
     o.pad = 0;
     a.rows[r] = o;
   }
-  const bool twice = block_or(x >= 0 && !first ? 1 : 0, redi) != 0;   // (uniform)
   if (x >= 0) {
     double ps = p;
-    if (twice) {
+    if (twice[0] | twice[1] | twice[2] | twice[3]) {   // a token stands in the list twice
       ps = 0.0;
       for (int j = 0; j < a.K; ++j) ps += lx[j] == x ? lp[j] : 0.0;
     }

@@ -183,8 +183,9 @@ def test_distill_sizes(R, V, K, T, tail, dt):
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("tail", [True, False])
-def test_distill_lists_and_masks(tail, dt):
-    """Empty, partly padded and doubled lists, tokens out of range, logits of -inf in them; student
+@pytest.mark.parametrize("times", [1, 33])
+def test_distill_lists_and_masks(tail, dt, times):
+    """(33 times over: enough rows that each workgroup takes whole ones.)  Empty, partly padded and doubled lists, tokens out of range, logits of -inf in them; student
     rows that are masked in part, in the list, off the list or wholly; NaN and +inf rows, in rows
     that count and in rows that do not."""
     R, V, K = 16, 10000, 12
@@ -214,7 +215,25 @@ def test_distill_lists_and_masks(tail, dt):
     w = torch.ones(R)
     w[13] = 0.0
     w[15] = 0.0
-    check_distill(s.to(DEV), index, t, lz, 1.0, w)
+    lz = None if lz is None else lz.repeat(times)
+    check_distill(s.repeat(times, 1).to(DEV), index.repeat(times, 1), t.repeat(times, 1), lz, 1.0, w.repeat(times))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("R,V,K", [(512, 5, 3), (515, 8, 8), (600, 4099, 40), (1100, 16389, 256)])
+def test_distill_whole_rows(R, V, K, dt):
+    """Enough rows that each workgroup takes whole ones: vocabularies of less than a vector, of one and
+    of an odd number, rows off the 16-byte grid, in place and not."""
+    note(f"case distill whole rows R={R} V={V} K={K} {dt}")
+    base = rows_of(37, V, dt, V)
+    index, t, lz = teacher_of(base, K, 1.0, V, True)
+    rep = torch.arange(R) % 37
+    w = torch.from_numpy(np.random.default_rng(1).uniform(-1, 2, R).astype(np.float32))
+    wide = torch.full((R, V + 3), float("nan"), dtype=dt, device=DEV)
+    for in_place in (False, True):
+        wide[:, 1:1 + V] = base[rep].to(DEV)
+        check_distill(wide[:, 1:1 + V], index[rep].contiguous(), t[rep].contiguous(), lz[rep].contiguous(), 1.0, w, in_place=in_place)
+    assert torch.isnan(wide[:, 0]).all() and torch.isnan(wide[:, 1 + V:]).all()
 
 
 def test_distill_far_apart():
