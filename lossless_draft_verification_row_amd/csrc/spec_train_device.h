@@ -77,8 +77,12 @@ __device__ __forceinline__ void tr_load(const void* p, int n, float (&v)[kTrPer]
 __device__ __forceinline__ float tr_sum_exp(const float (&v)[kTrPer], float m, float c) {
   float s = 0.f;
   if (m > -INFINITY) {
+    float p[4] = {0.f, 0.f, 0.f, 0.f};   // (no exponential's result is needed by the next instruction)
 #pragma unroll
-    for (int j = 0; j < kTrPer; ++j) s += __builtin_amdgcn_exp2f((v[j] - m) * c);
+    for (int j = 0; j < kTrPer; j += 4)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) p[q] += __builtin_amdgcn_exp2f((v[j + q] - m) * c);
+    s = (p[0] + p[1]) + (p[2] + p[3]);
   } else {
 #pragma unroll
     for (int j = 0; j < kTrPer; ++j)
