@@ -357,7 +357,8 @@ size_t spec_row_topk_workspace_bytes(int R, int V, int K);
  *          token"): L = sum_j p_j (ln p_j - ln q(x_j)) + rho (ln rho - ln q_rho); with
  *          M = sum_j p_j + rho,  dL/ds_v = (M q_v - sum_{x_j = v} p_j) / T for a listed v and
  *          (M - rho / q_rho) q_v / T for another.  A rho up to 2^-20 counts as 0 (the rounding of
- *          an fp32 log Z); if rho > 0 and q_rho = 0 the loss is +inf and those logits' gradient 0.
+ *          an fp32 log Z up to 16; of a larger one, as at low temperatures, 2^-24 |log Z| of it is
+ *          rounding, and a list that holds all the mass is better given without it); if rho > 0 and q_rho = 0 the loss is +inf and those logits' gradient 0.
  *  row_weight  [R] fp32 or NULL (1).
  *  out_loss    [R] fp32; out_log_z [R] fp32 or NULL: the student's ln sum_v exp(s_v / T).
  *  d_logits    [R, V] of the logits' type, row stride d_ld, or NULL (no gradient).  May be `logits`
@@ -387,7 +388,8 @@ size_t spec_topk_distill_workspace_bytes(int R, int V, int K, int grad);
  * The vocabulary is taken in pieces: the workspace, spec_lm_head_loss_workspace_bytes(R, V, D,
  * d_hidden || d_weight) bytes, 256-byte aligned, holds the logits' gradient (bf16) of one piece,
  * at most 256 MB or 256 columns.  The logits carry fp32 accumulation error (at most
- * D 2^-24 sum_d |h_d W_vd|), the gradients bf16 rounding of the logits' gradient and of the result.
+ * D 2^-24 sum_d |h_d W_vd|), the gradients bf16 rounding of the logits' gradient and of the result;
+ * a probability's own error is up to 2^-40 besides, so that smaller ones may count as 0.
  * A NaN or +inf logit, or no finite one, makes the row's loss NaN, and NaN spreads to the
  * gradients that the row enters (all of d_weight) unless the row is left out. */
 int spec_lm_head_loss(int R, int V, int D, const void* hidden, int64_t h_ld, const void* weight, int64_t w_ld,

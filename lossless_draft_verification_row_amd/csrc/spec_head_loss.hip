@@ -166,7 +166,10 @@ struct HlCore {
   static __device__ __forceinline__ void mma(f32x4& c, const bf16x8& a, const bf16x8& b) {
     asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
-  static __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+  static __device__ __forceinline__ void settle() {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
   // The first product of a tile: c = a b, so that nothing has to be cleared before.
   static __device__ __forceinline__ void mma_first(f32x4& c, const bf16x8& a, const bf16x8& b) {
     asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
@@ -296,7 +299,9 @@ struct HlCore {
   static __device__ __forceinline__ void begin(Buf& b0, Buf& b1, const HlOperand& A, const HlOperand& B, const Wave& w,
                                                int n_k, int k_len) {
     loads(b0, A, B, w, 0, n_k, k_len, 0, NA + NB);
+    __builtin_amdgcn_sched_barrier(0);   // run() counts on this order
     loads(b1, A, B, w, 1, n_k, k_len, 0, NA + NB);
+    __builtin_amdgcn_sched_barrier(0);
   }
   // A tile whose begin() has been: n_k stages (an odd number is followed by one of zeros); k_len
   // (of a k-contiguous operand) beyond which k reads as zero.  Where n_k is 0 the result is 0.  With
@@ -429,10 +434,9 @@ __device__ __forceinline__ void prepare_row(const HlArgs& a, int block, int grad
   if (lane == 0) {
     a.ly[r] = s;
     HlRow o;
-    o.lz2 = 0.f;
+    o.m = o.l2 = 0.f;
     o.scale = (float)((double)w * a.inv_t);
     o.y = y;
-    o.pad = 0;
     a.rows[r] = o;
   }
 }
@@ -510,7 +514,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
       (wave & 2 ? b1.a : b0.a) + (wave & 1) * 32 * TI * TJ, lane, n_vp - (v0 - keep) - vw,
       [&](int i, int j) {
         // fp16 of 2^15 e: 11 bits down to 2^-29 of the wave's maximum, so that G's own rounding to
-        // bf16 is the only one that counts
+        // bf16 is the only one that counts; below, steps of 2^-39 of a probability, where bf16 would
+        // round each of the others twice
         return u32x2{pack_f16(acc[i][j][0] * kKeepScale, acc[i][j][1] * kKeepScale),
                           pack_f16(acc[i][j][2] * kKeepScale, acc[i][j][3] * kKeepScale)};
       },
@@ -565,7 +570,8 @@ __global__ __launch_bounds__(kThreads) void k_hl_rows(HlArgs a, int n_rec) {
   const double lz = (double)m * a.inv_t + l2 * 0.6931471805599453;
   if (a.log_z) a.log_z[r] = (float)lz;
   if (a.loss) a.loss[r] = a.rows[r].y < 0 ? 0.f : (float)(lz - (double)a.ly[r] * a.inv_t);
-  a.rows[r].lz2 = (float)((double)m * (double)a.c + l2);
+  a.rows[r].m = m;
+  a.rows[r].l2 = (float)l2;
 }
 
 // Exponentials -> G of the last piece, in place, 32 bytes a thread: columns keep .. V - 1 and on
@@ -581,7 +587,7 @@ __global__ __launch_bounds__(kThreads) void k_hl_scale(HlArgs a, int keep, int c
   if (row.scale != 0.f) {
     const float m = a.rec[(int64_t)((keep + v) / cols) * a.plan.Rp + r].x;
     // 2^-15 e^(m / T) / Z: nothing if the record's maximum is -inf (and NaN where Z is)
-    const float f = __builtin_amdgcn_exp2f(fmaf(m, a.c, -row.lz2)) * (1.f / kKeepScale);
+    const float f = __builtin_amdgcn_exp2f(fmaf(m - row.m, a.c, -row.l2)) * (1.f / kKeepScale);
     const int y = row.y - keep - v;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -620,14 +626,15 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
   Core::run_one(b0, b1, A, B, (a.D + kHlDepth - 1) / kHlDepth, a.D, acc);
   const int n_vp = (n_v + kHlDepth - 1) / kHlDepth * kHlDepth;
   const int vw = 16 * TI * wr;                        // the wave's first column within the tile
-  float lz2[TJ], scale[TJ];
+  float m[TJ], l2[TJ], scale[TJ];
   int y[TJ];                                          // target, from the lane's first column on
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
     const int r = r0 + 16 * (TJ * wc + j) + (lane & 15);
-    HlRow row = {0.f, 0.f, -1, 0};
+    HlRow row = {0.f, 0.f, 0.f, -1};
     if (r < a.plan.Rp) row = a.rows[r];
-    lz2[j] = row.lz2;
+    m[j] = row.m;
+    l2[j] = row.l2;
     scale[j] = row.scale;
     y[j] = row.y - (v0 + vw + 4 * (lane >> 4));
   }
@@ -639,7 +646,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], a.c, -lz2[j]));
+          // (from the difference, whose size does not grow with the logits' or with 1 / T)
+          const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e] - m[j], a.c, -l2[j]));
           x[e] = (y[j] == 16 * i + e ? p - 1.f : p) * scale[j];
           if (scale[j] == 0.f || 16 * i + e >= v_left) x[e] = 0.f;
         }

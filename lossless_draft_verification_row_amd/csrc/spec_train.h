@@ -14,10 +14,9 @@ constexpr int kHlTile = 256;      // vocabulary columns (and features) per tile
 constexpr int kHlDepth = 64;      // k per stage
 
 struct HlRow {                    // what the gradient tiles need of a row
-  float lz2;                      // log2 sum 2^(l c)
+  float m, l2;                    // largest logit, log2 sum 2^((l - m) c)
   float scale;                    // row weight / T; 0: the row is left out
   int y;                          // target, -1: none
-  int pad;
 };
 
 // How a call is cut up; the same on the host for the workspace's size and for the launches.

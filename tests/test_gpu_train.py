@@ -397,6 +397,88 @@ def test_head_loss_strided_with_nan_padding():
     assert (dh[:, D:] == 7).all() and (dw[:, :8] == 7).all() and (dw[0] == 7).all() and (dw[-1] == 7).all()
 
 
+@pytest.mark.parametrize("T", [0.01, 1e-30, 50.0])
+def test_temperatures_far_from_one(T):
+    """Sharp and flat distributions; at 1e-30 the distances alone stay in fp32's range."""
+    T = float(np.float32(T))   # what the entry points take: 0.01 itself is 2e-8 off it, times log Z = 1500
+    l = rows_of(4, 9000, BF, 31).to(DEV)
+    check_topk(l, 20, T)
+    index, t, lz = teacher_of(l, 20, T, 3, True) if T > 1e-3 else (*teacher_of(l, 20, 1.0, 3, False)[:2], None)
+    if T > 1e-3:
+        check_distill(l, index, t, lz, T, None)
+    h, wt, y = head_of(70, 900, 64, 41)
+    if T > 1e-3:
+        check_head(h, wt, y, T, None)
+    else:
+        # one-hot at the largest logit: loss (max - l_y) / T, gradients of one token against another
+        best = (h.double() @ wt.double().T).argmax(dim=1).int()
+        w = torch.full((70,), T)
+        res = L.spec_lm_head_loss(h, wt, best, temperature=T, row_weight=w.to(DEV), grad=True)
+        other = (best + 1) % 900
+        res2 = L.spec_lm_head_loss(h, wt, other, temperature=T, row_weight=w.to(DEV), grad="hidden")
+        torch.cuda.synchronize()
+        assert (res["d_hidden"] == 0).all() and (res["d_weight"] == 0).all()
+        ref = wt[best.long()].double() - wt[other.long()].double()
+        off = (res2["d_hidden"].double() - ref).abs() - (2 * O.U * wt.double().abs().sum(dim=0) + O.HALF[BF] * ref.abs())
+        assert float(off.max()) <= 0
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits, and a head of more than 2^31 weights: the far ends are right."""
+    R, V, K = 14200, 151936, 8
+    note(f"case offsets R={R} V={V}")
+    l = torch.zeros((R, V), dtype=BF, device=DEV)
+    far = rows_of(3, V, BF, 5)
+    l[-3:] = far.to(DEV)
+    rec = L.spec_row_topk(l, K)
+    index, logit, log_z = O.topk(n64(far), K, 1.0)
+    np.testing.assert_array_equal(rec["index"][-3:].cpu().numpy(), index)
+    np.testing.assert_array_equal(rec["index"][:2].cpu().numpy(), np.arange(K)[None].repeat(2, 0))
+    i, t, lz = teacher_of(far, K, 1.0, 2, True)
+    big = [v.new_zeros((R,) + tuple(v.shape[1:])) for v in (i, t, lz)]
+    big[0].fill_(-1)
+    for b, v in zip(big, (i, t, lz)):
+        b[-3:] = v
+    big = [b.to(DEV) for b in big]
+    res = L.spec_topk_distill(l, big[0], big[1], teacher_log_z=big[2], grad=True, out={"d_logits": l})
+    torch.cuda.synchronize()
+    loss, _, d, e_loss, e_d = O.distill(n64(far), i.numpy(), t.numpy(), n64(lz), 1.0, None)
+    within(n64(res["loss"][-3:]), loss, e_loss, "loss")
+    within(n64(l[-3:]), d, e_d + O.HALF[BF] * (np.abs(d) + e_d), "d_logits")
+    assert (res["loss"][:-3] == 0).all() and not l[:-3].any()
+    del l, res, rec
+    V, D = 1 << 21, 1032
+    note(f"case offsets head V={V} D={D}")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    wt = torch.empty((V, D), dtype=BF, device=DEV).normal_(0, 0.04, generator=g)
+    h = torch.randn((3, D), generator=g, device=DEV).to(BF)
+    y = torch.tensor([V - 1, 5, -1], dtype=torch.int32, device=DEV)
+    res = L.spec_lm_head_loss(h, wt, y, grad=True)
+    torch.cuda.synchronize()
+    lz, dh = torch.full((3,), -np.inf, dtype=torch.float64, device=DEV), torch.zeros((3, D), dtype=torch.float64, device=DEV)
+    for a in range(0, V, 1 << 18):
+        lz = torch.logaddexp(lz, torch.logsumexp(h.double() @ wt[a:a + (1 << 18)].double().T, dim=1))
+    ly = (h[:2].double() * wt[y[:2].long()].double()).sum(dim=1)
+    delta = float(D * O.U * (h.double().abs().sum(dim=1) * 0.25).max())     # |w| < 0.25: six deviations
+    assert (res["loss"][:2].double() - (lz[:2] - ly)).abs().max() <= 2 * delta + 2 * O.LZ + 4 * O.U * 20
+    for a in range(0, V, 1 << 18):
+        w = wt[a:a + (1 << 18)].double()
+        p = torch.exp(h.double() @ w.T - lz[:, None])
+        p[2] = 0.0
+        dh += p @ w
+        for r in (0, 1):
+            if a <= int(y[r]) < a + (1 << 18):
+                p[r, int(y[r]) - a] -= 1.0
+        ref = p.T @ h.double()
+        got = res["d_weight"][a:a + (1 << 18)].double()
+        e = p.abs().T @ h.double().abs() * (2 * O.HALF[BF] + 2 * delta + 4 * O.LZ + 1e-4) + 2.0 ** -133
+        assert float(((got - ref).abs() - e).max()) <= 0, a
+    dh[:2] -= wt[y[:2].long()].double()
+    dh[2] = 0.0
+    # the probabilities' roundings to bf16 are spread over 2^21 tokens: their sum against |w| < 0.25
+    assert float((res["d_hidden"].double() - dh).abs().max()) <= 0.25 * (O.HALF[BF] + 2 * delta + 1e-4) + O.HALF[BF] * float(dh.abs().max())
+
+
 def test_head_loss_one_gradient_at_a_time_and_no_rows():
     h, wt, y = head_of(90, 1200, 128, 3)
     both = L.spec_lm_head_loss(h, wt, y.to(DEV), grad=True)

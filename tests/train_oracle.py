@@ -116,10 +116,13 @@ def head(h, wt, y, T, w):
     yy = torch.where(keep, y, 0)
     loss = torch.where(keep, lz - l.gather(1, yy[:, None])[:, 0], 0.0)
     p = torch.exp(l - lz[:, None])
-    # exponents are formed as l c - log2 Z: 2 u of each of the two
+    # exponents are formed as (l - m) c - log2 sum: no more than 2 u of each of l c and log2 Z
     e_rel = (2 * delta + 2 * LZ)[:, None] + 4 * U * (l.abs() + lz.abs()[:, None])
     scale = torch.where(used, w, 0.0)[:, None] / T
-    e_p = torch.where(used[:, None], p * e_rel * scale.abs(), 0.0)
+    # Exponentials may be kept as fp16 of 2^15 e, e <= 1: below 2^-29 the step of e is fp16's
+    # smallest, 2^-24 / 2^15, half of which is 2^-40; e / Z is off by no more, as Z >= 1 where e <= 1
+    # is the distance from the row's maximum, and a wave's lower maximum scales both down.
+    e_p = torch.where(used[:, None], (p * e_rel + 2.0 ** -40) * scale.abs(), 0.0)
     g = torch.where(used[:, None], p * scale, 0.0)
     g.scatter_add_(1, yy[:, None], -scale)
     # G is rounded to bf16
