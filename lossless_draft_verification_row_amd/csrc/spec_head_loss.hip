@@ -445,6 +445,12 @@ __device__ __forceinline__ void prepare_row(const HlArgs& a, int block, int grad
 
 // The first n_tiles workgroups take logit tiles, the others four rows each.  `keep` is the first
 // column of the piece whose exponentials are kept (V: none).
+//
+// Bound by the matrix cores, beyond some 250 rows: 512 rows, V = 151,936, D = 4096 take 532 to 537 us,
+// 1.19 PFLOP/s (4.64 rounds of tiles in 5); 4096 rows, V = 128,256, 3.4 to 3.6 ms, 1.18 to 1.25.  With
+// zeros for operands these are 1.36 and 1.64: the power that the data costs is most of the rest.
+// 64 rows, V = 32,003, D = 1024: 18 us, one tile per workgroup and half of the CUs.  The tile's height
+// follows the rows (hl_plan), so that 448 rows do no more products than two tiles of 224 have.
 template <int TI, int TJ, int WRN>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_stats(HlArgs a, int n_rt,
                                                                                                  int n_tiles, int keep) {
@@ -534,7 +540,8 @@ __device__ __forceinline__ void take_in(float& m, double& s, float mo, double so
   m = mx;
 }
 
-// Four rows per workgroup, 64 threads to a row: the waves' records, folded in fp64.
+// Four rows per workgroup, 64 threads to a row: the waves' records, folded in fp64.  Latencies: 4 us for
+// 64 rows, 9 us for 448, 24 us for 4096 (33 MB of records).
 __global__ __launch_bounds__(kThreads) void k_hl_rows(HlArgs a, int n_rec) {
   __shared__ float sm[kWaves][4];
   __shared__ double ss[kWaves][4];
@@ -578,7 +585,8 @@ __global__ __launch_bounds__(kThreads) void k_hl_rows(HlArgs a, int n_rec) {
 
 // Exponentials -> G of the last piece, in place, 32 bytes a thread: columns keep .. V - 1 and on
 // to the next multiple of 64 (whose exponentials are 0), rows 0 .. Rp - 1.  `cols` columns
-// share a record (one wave's of a tile).
+// share a record (one wave's of a tile).  Bound by memory: 448 rows of 151,936 (272 MB read and
+// written) in 54 us, 5.0 TB/s; forming them again would be 500 us of products.
 __global__ __launch_bounds__(kThreads) void k_hl_scale(HlArgs a, int keep, int cols, int n_chunk) {
   const int r = blockIdx.x / n_chunk, v = ((blockIdx.x - r * n_chunk) * kThreads + (int)threadIdx.x) * 16;
   const int n_vp = (a.V - keep + kHlDepth - 1) / kHlDepth * kHlDepth;
@@ -612,6 +620,8 @@ __global__ __launch_bounds__(kThreads) void k_hl_scale(HlArgs a, int keep, int c
 
 // G of one piece: columns v0 .. v0 + n_v - 1 (n_v a multiple of 64 but for the vocabulary's end;
 // the columns up to the next multiple of 64 are written as zeros, as are rows R .. Rp - 1).
+// k_hl_stats' product with another epilogue: 4096 rows, 32,768 columns, D = 4096 in 0.87 to 0.9 ms,
+// 1.22 to 1.26 PFLOP/s.
 template <int TI, int TJ, int WRN>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_grad(HlArgs a, int pv0,
                                                                                                 int n_v, int n_rt) {
@@ -653,7 +663,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
           x[e] = (y[j] == 16 * i + e ? p - 1.f : p) * scale[j];
           if (scale[j] == 0.f || 16 * i + e >= v_left) x[e] = 0.f;
         }
-        // G is rounded to bf16 (half a step, 2^-9 of each entry): both products take bf16
+        // G is rounded to bf16 (half a step, 2^-8 of each entry): both products take bf16
         // operands, and the errors of a row's entries are independent
         return u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
       },
@@ -661,6 +671,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
 }
 
 // dh[r][d] over columns of the piece: k = v, A = W (k major, rows d), B = G (k contiguous).
+// The result is small and k is long, so k is split until every CU has a workgroup; each split adds up
+// its fp32 part over the pieces.  4096 rows and 32,768 columns, D = 4096: 0.72 to 0.81 ms, 1.36 to
+// 1.52 PFLOP/s; 448 rows, all 151,936 columns: 457 to 526 us, 1.06 to 1.22.
 template <int TI, int TJ, int WRN>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_hl_dhidden(
     HlArgs a, int pv0, int n_v, int n_rt, int n_dt, int add) {
@@ -708,7 +721,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
 // With few rows a tile's product is short against what surrounds it (448 rows: 7 us of MFMAs, 15 us
 // of waiting for the first loads and of storing 128 KB), so each CU's workgroup goes through tiles
 // with the next one's first two stages on their way while this one's result leaves, through LDS of
-// its own, and does not wait for the stores before its third stage.
+// its own, and does not wait for the stores before its third stage.  448 rows, V = 151,936, D = 4096:
+// 0.67 to 0.82 ms with 1.24 GB of stores (0.14 more with a workgroup to each tile); 4096 rows and 32,768
+// columns 0.76 to 0.80 ms, 1.38 to 1.46 PFLOP/s.
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_hl_dweight(
     HlArgs a, int pv0, int n_v, int n_dt, int n_tiles) {
   constexpr int TI = 8, TJ = 8, WRN = 2, kStores = 32;
@@ -779,7 +794,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   }
 }
 
-// d_hidden = the splits' parts, added in order, rounded once.
+// d_hidden = the splits' parts, added in order, rounded once.  Bound by memory: 8 us for 333 rows of
+// 1032, 23 us for 448 of 4096 (59 MB of parts).
 __global__ __launch_bounds__(kThreads) void k_hl_reduce(HlArgs a) {
   const int64_t n4 = (int64_t)a.R * (a.D / 4), i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n4) return;

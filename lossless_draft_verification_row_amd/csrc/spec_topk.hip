@@ -76,6 +76,12 @@ __device__ __forceinline__ uint32_t wave_kth(const uint32_t (&key)[NM], int kk) 
   return prefix;
 }
 
+// One read of the row and no write of its size: the floor is the read.  512 bf16 rows of 151,936
+// (156 MB) take 45 us, 3.5 TB/s: per logit an unpacking, a maximum, an exponential with its
+// subtraction, multiplication and sum, and a comparison have to be issued, which 2-byte logits do
+// not leave the time for.  1027 fp32 rows of 32,003 (131 MB) take 30 us, 4.4 TB/s.  A row is cut
+// into segments of equal length, so that no workgroup has a short one, of at most 32 logits a
+// thread, which stay in registers between the maximum, the sum and the selection.
 template <int DT, int NM>
 __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
   __shared__ uint32_t wb[2][kWaves];
@@ -220,6 +226,8 @@ __device__ __forceinline__ void each_candidate(const TopkArgs& a, const uint64_t
   }
 }
 
+// A few thousand candidates a row, so that latencies are what it takes: 7 us for one row, 12 us for
+// 512 (top 64), 14.5 us for 1027 (top 128).
 template <int NM>
 __global__ __launch_bounds__(kThreads) void k_tk_merge(TopkArgs a) {
   __shared__ alignas(16) uint64_t key[kMergeCap + kRankStep];
