@@ -763,7 +763,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
       place(i);
       Core::begin(b0, b1, A, B, w, n_k, a.plan.Rp);
     }
-    // kStores stores, whatever of them lies outside the matrix or the piece (their offsets do too)
+    // kStores stores, whatever of them lies outside the matrix or the piece (their offsets do too),
+    // marked as not read again: kept, an XCD's 4 MB of results a round put G and h out of its L2
+    // (448 rows: 1.20 GB read again, with the mark 0.78; the call 1763 us, with the mark 1704)
     const __amdgpu_buffer_rsrc_t rs =
         stage_rsrc({a.d_weight + (int64_t)(pv0 + vw) * a.dw_ld + dw, a.dw_ld, extent(a.V, a.D, a.dw_ld, pv0 + vw, dw)}, 0, 0);
     uint4* o = out[wave];
@@ -786,7 +788,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
         const u32x4 v = *(const u32x4*)&o[r * 16 + (g ^ (r & 15))];
         const bool in = vw + row < n_v && dw + 8 * g < a.D;
         const int off = in ? (int)(row * a.dw_ld * 2) + 16 * g : kFarOffset;
-        __builtin_amdgcn_raw_buffer_store_b128(v, rs, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(v, rs, off, 0, 2);
       }
       wave_sync();
     }
