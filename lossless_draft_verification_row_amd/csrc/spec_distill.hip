@@ -24,6 +24,7 @@
 namespace specv {
 
 constexpr int kTdPer = kTrSeg / kThreads;   // 32 logits per thread
+constexpr int64_t kTdPast = 1 << 27;        // bytes
 constexpr double kTdTailMin = 0x1p-20;      // mass off the list that counts: below it is the
                                             // rounding of an fp32 log Z
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ void td_put(void* row, int i, float x) {
   else ((float*)row)[i] = x;
 }
 // The first n of a segment's logits to p, in tr_load's order.
-template <int DT>
+template <int DT, bool PAST>
 __device__ __forceinline__ void td_store(void* p, int n, const float (&v)[kTdPer]) {
   constexpr int kEl = TrEl<DT>::n;
 #pragma unroll
@@ -58,7 +59,7 @@ __device__ __forceinline__ void td_store(void* p, int n, const float (&v)[kTdPer
       else
         x = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
                        __float_as_uint(v[4 * q + 3]));
-      st16_any((char*)p + (int64_t)e0 * (16 / kEl), x);
+      st16_any<PAST>((char*)p + (int64_t)e0 * (16 / kEl), x);
     } else {
 #pragma unroll
       for (int e = 0; e < kEl; ++e)
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void k_td_loss(DistillArgs a) {
 // 6.5 TB/s; a copy of that size reaches 5.2 to 5.6.  Reading a row a second time is the price of log Z:
 // one workgroup that keeps to one row and finds it in the caches was no faster (351 us against 350 for
 // the three kernels), nor were groups of rows (128 to 1024: 510 to 348 us).
-template <int DT>
+template <int DT, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_td_grad(DistillArgs a) {
   const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * a.seg, n = min(a.seg, a.V - base);
   constexpr int kSz = 16 / TrEl<DT>::n;   // bytes of a logit
@@ -245,13 +246,13 @@ __global__ __launch_bounds__(kThreads) void k_td_grad(DistillArgs a) {
   if (row.zero) {
 #pragma unroll
     for (int j = 0; j < kTdPer; ++j) v[j] = 0.f;
-    td_store<DT>(out, n, v);
+    td_store<DT, PAST>(out, n, v);
     return;
   }
   tr_load<DT>((const char*)row_ptr<DT>(a.logits, a.ld, r) + (int64_t)base * kSz, n, v);
 #pragma unroll
   for (int j = 0; j < kTdPer; ++j) v[j] = __builtin_amdgcn_exp2f((v[j] - row.m) * a.c) * row.f;
-  td_store<DT>(out, n, v);
+  td_store<DT, PAST>(out, n, v);
   wait_vmem();       // the list's tokens are written over what this stored
   __syncthreads();
   float tl;
@@ -265,7 +266,13 @@ void topk_distill(const DistillArgs& a, hipStream_t st) {
   const dim3 segs((unsigned)(a.R * a.n_seg)), block(kThreads);
   hipLaunchKernelGGL((k_td_stats<DT>), segs, block, 0, st, a);
   hipLaunchKernelGGL((k_td_loss<DT>), dim3((unsigned)a.R), block, 0, st, a);
-  if (a.d_logits) hipLaunchKernelGGL((k_td_grad<DT>), segs, block, 0, st, a);
+  if (!a.d_logits) return;
+  // A gradient that is a good part of the memory-side cache (256 MB) or more goes past it: 2048 rows of
+  // 151,936 in bf16 312 us (343 by way of it), 512 rows (156 MB) 88 (92), 2048 rows of 32,000 (131 MB)
+  // 85 (90).  A smaller one stays where its reader finds it: 256 rows of 151,936 (78 MB) 50 us (51 past
+  // it), 512 fp32 rows of 32,000 (66 MB) 43 (45).
+  if (a.R * (int64_t)a.V * (16 / TrEl<DT>::n) > kTdPast) hipLaunchKernelGGL((k_td_grad<DT, true>), segs, block, 0, st, a);
+  else hipLaunchKernelGGL((k_td_grad<DT, false>), segs, block, 0, st, a);
 }
 }  // namespace
 

@@ -24,9 +24,11 @@ __device__ __forceinline__ uint4 ld16_any(const void* p) {
   const u32x4_any w = __builtin_nontemporal_load((const u32x4_any*)p);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+template <bool PAST>   // PAST: not to be read again soon
 __device__ __forceinline__ void st16_any(void* p, uint4 x) {
   const u32x4_any w = {x.x, x.y, x.z, x.w};
-  *(u32x4_any*)p = w;
+  if constexpr (PAST) __builtin_nontemporal_store(w, (u32x4_any*)p);
+  else *(u32x4_any*)p = w;
 }
 
 // This thread's 32 logits of the n logits at p: 16-byte vectors dealt round-robin over the
