@@ -114,18 +114,11 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
   // logits of -inf are no candidates; the bound's 16 bits stand for the least key that has them
   float thr = tk_value(b << 16);
   if (!(thr >= -0x1.fffffep127f)) thr = -0x1.fffffep127f;
-  // each thread's candidates, and their places by a sum over the lanes
+  // the wave's candidates (counted on the scalar unit)
   int n = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) n += v[j] >= thr ? 1 : 0;
-  int at = n;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(at, d);
-    at += lane >= d ? o : 0;
-  }
-  if (lane == 63) red[wave] = at;
-  at -= n;
+  for (int j = 0; j < kPer; ++j) n += __popcll(__ballot(v[j] >= thr));
+  if (lane == 0) red[wave] = n;
   __syncthreads();
   int total = red[0] + red[1] + red[2] + red[3];
   uint64_t* out = a.cand + slot * a.cap;
@@ -187,12 +180,21 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
     if (threadIdx.x == 0) a.n_cand[slot] = min(count, a.cap);
     return;
   }
+  // a register's candidates stand together, by lane
+  int at = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) at += w < wave ? red[w] : 0;
-  out += at;
+  out += __builtin_amdgcn_readfirstlane(at);
+  asm volatile("" : "+v"(thr));   // (the comparisons are made again, not kept in scalar registers)
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (v[j] >= thr) *out++ = ((uint64_t)tk_key(v[j]) << 32) | (uint32_t)~(base + tk_index<DT>(j));
+  for (int j = 0; j < kPer; ++j) {
+    const uint64_t b = __ballot(v[j] >= thr);
+    if (b) {   // uniform
+      const uint32_t i = __builtin_amdgcn_mbcnt_hi((uint32_t)(b >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)b, 0));
+      if (v[j] >= thr) out[i] = ((uint64_t)tk_key(v[j]) << 32) | (uint32_t)~(base + tk_index<DT>(j));
+      out += __popcll(b);
+    }
+  }
   if (threadIdx.x == 0) a.n_cand[slot] = total;
 }
 

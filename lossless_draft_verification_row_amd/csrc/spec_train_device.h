@@ -72,19 +72,29 @@ __device__ __forceinline__ void tr_load(const void* p, int n, float (&v)[kTrPer]
     }
 }
 
-// sum of 2^((v - m) c) over this thread's logits, m their (or the wave's) maximum.  The difference
-// comes first: it is exactly 0 at the maximum, whereas v c - fl(m c) in one fma would leave the
-// rounding of m c, which has no bound for large logits.  m = +inf gives NaN; with m = -inf the sum
-// is 0, or NaN where fmaxf has passed over one.
+// sum of 2^((v - m) c) over this thread's logits, m their wave's maximum: v c - fl(m c) in one fma
+// (an operation a logit less than a difference and a product), whose terms share the rounding of
+// m c, an exact fma of its own, taken off the sum.  For large m c, where that rounding has no bound
+// that an exponential bears, the difference comes first.  m = +inf gives NaN; with m = -inf the
+// sum is 0, or NaN where fmaxf has passed over one.
 __device__ __forceinline__ float tr_sum_exp(const float (&v)[kTrPer], float m, float c) {
   float s = 0.f;
   if (m > -INFINITY) {
     float p[4] = {0.f, 0.f, 0.f, 0.f};   // (no exponential's result is needed by the next instruction)
+    const float mc = m * c;
+    if (__builtin_expect(fabsf(mc) < 0x1p20f, 1)) {   // uniform; the rounding is below 2^-4
 #pragma unroll
-    for (int j = 0; j < kTrPer; j += 4)
+      for (int j = 0; j < kTrPer; j += 4)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) p[q] += __builtin_amdgcn_exp2f((v[j + q] - m) * c);
-    s = (p[0] + p[1]) + (p[2] + p[3]);
+        for (int q = 0; q < 4; ++q) p[q] += __builtin_amdgcn_exp2f(fmaf(v[j + q], c, -mc));
+      s = ((p[0] + p[1]) + (p[2] + p[3])) * __builtin_amdgcn_exp2f(-fmaf(m, c, -mc));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kTrPer; j += 4)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p[q] += __builtin_amdgcn_exp2f((v[j + q] - m) * c);
+      s = (p[0] + p[1]) + (p[2] + p[3]);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < kTrPer; ++j)
