@@ -77,7 +77,7 @@ __device__ __forceinline__ int td_token(const DistillArgs& a, int64_t r, int j, 
   return x >= 0 && x < a.V && t != -INFINITY ? x : -1;
 }
 
-// Bound by the read: 2048 bf16 rows of 151,936 (622 MB) in 102 us, 6.1 TB/s; 448 rows in 26 us,
+// Bound by the read: 2048 bf16 rows of 151,936 (622 MB) in 100 us, 6.2 TB/s; 448 rows in 26 us,
 // 5.2 TB/s.  8192 logits are 16 or 32 KB, all of whose loads are in flight before the first is used;
 // the list goes into a bit per logit in LDS meanwhile.
 template <int DT>
@@ -232,10 +232,11 @@ __global__ __launch_bounds__(kThreads) void k_td_loss(DistillArgs a) {
   }
 }
 
-// Bound by memory: 2048 bf16 rows of 151,936 are read and written (1.24 GB) in 190 to 225 us, 5.5 to
-// 6.5 TB/s; a copy of that size reaches 5.2 to 5.6.  Reading a row a second time is the price of log Z:
-// one workgroup that keeps to one row and finds it in the caches was no faster (351 us against 350 for
-// the three kernels), nor were groups of rows (128 to 1024: 510 to 348 us).
+// Bound by memory: 2048 bf16 rows of 151,936 are read and written (1.24 GB) in 189 to 193 us, 6.5
+// TB/s; a copy of that size reaches 5.2 to 5.6.  Reading a row a second time is the price of log Z:
+// one workgroup that keeps to one row and finds it in the caches was no faster (351 us, when the three
+// kernels took 350), nor were groups of rows (128 to 1024: 510 to 348 us), or the rows in reverse with
+// the first read kept (367 us, when they took 347).
 template <int DT, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_td_grad(DistillArgs a) {
   const int seg = blockIdx.x % a.n_seg, r = blockIdx.x / a.n_seg, base = seg * a.seg, n = min(a.seg, a.V - base);

@@ -722,7 +722,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
 // of waiting for the first loads and of storing 128 KB), so each CU's workgroup goes through tiles
 // with the next one's first two stages on their way while this one's result leaves, through LDS of
 // its own, and does not wait for the stores before its third stage.  448 rows, V = 151,936, D = 4096:
-// 0.67 to 0.82 ms with 1.24 GB of stores (0.14 more with a workgroup to each tile); 4096 rows and 32,768
+// 0.65 to 0.76 ms with 1.24 GB of stores (0.14 more with a workgroup to each tile); 4096 rows and 32,768
 // columns 0.76 to 0.80 ms, 1.38 to 1.46 PFLOP/s.
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_hl_dweight(
     HlArgs a, int pv0, int n_v, int n_dt, int n_tiles) {

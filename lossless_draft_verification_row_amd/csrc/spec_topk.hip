@@ -5,8 +5,9 @@
 //               and every logit that can be among the row's k largest
 //   k_tk_merge  one workgroup per row: the segments' candidates -> the k largest, in order
 //
-// A candidate's 64-bit key holds its order key (a larger logit, a larger key; -0 counts as +0)
-// above the complement of its index, so that keys are distinct and equal logits rank by index.
+// A candidate is stored as its logit above the complement of its index.  Its 64-bit key has an order
+// key (a larger logit, a larger key; -0 counts as +0) in the logit's place, so that keys are distinct
+// and equal logits rank by index.
 // What reaches a bound that at least k of a segment's per-thread maxima reach holds the segment's
 // k largest logits, and for a row without order few more.  Each wave finds the ceil(k / 4)-th
 // largest of its 64 maxima (of each thread's two largest for k > 128) to 16 bits by ballots; the
@@ -33,7 +34,12 @@ __device__ __forceinline__ uint32_t tk_key(float v) {
 __device__ __forceinline__ float tk_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
-constexpr uint32_t kKeyNegInf = 0x007fffffu;   // tk_key(-inf)
+__device__ __forceinline__ uint64_t tk_pack(float v, uint32_t not_index) {
+  return (uint64_t)__float_as_uint(v) << 32 | not_index;
+}
+__device__ __forceinline__ uint64_t tk_key_of(uint64_t packed) {
+  return (uint64_t)tk_key(__uint_as_float((uint32_t)(packed >> 32))) << 32 | (uint32_t)packed;
+}
 
 // Index within the segment of register j of this thread (tr_load's order).
 template <int DT>
@@ -77,9 +83,11 @@ __device__ __forceinline__ uint32_t wave_kth(const uint32_t (&key)[NM], int kk) 
 }
 
 // One read of the row and no write of its size: the floor is the read.  512 bf16 rows of 151,936
-// (156 MB) take 45 us, 3.5 TB/s: per logit an unpacking, a maximum, an exponential with its
-// subtraction, multiplication and sum, and a comparison have to be issued, which 2-byte logits do
-// not leave the time for.  1027 fp32 rows of 32,003 (131 MB) take 30 us, 4.4 TB/s.  A row is cut
+// (156 MB) take 41 us, 3.8 TB/s, 1027 fp32 rows of 32,003 (131 MB) 29 us, 4.6 TB/s: vector issue, some
+// 85 % of the time busy (per logit an unpacking, a maximum, fma, exponential and sum, and two
+// comparisons), in six waves a SIMD whose loads come before all of it.  What a candidate costs
+// counts too, as most registers of a wave hold one: it is stored as it is and gets its key in the
+// merge (key here: 44.5 us); with 124 registers, four waves, it is 50 us.  A row is cut
 // into segments of equal length, so that no workgroup has a short one, of at most 32 logits a
 // thread, which stay in registers between the maximum, the sum and the selection.
 template <int DT, int NM>
@@ -173,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
       // (a NaN's key may pass: its row is not listed, but the list must not overflow)
       if ((k >> kSh) > (lo >> kSh) || ((k >> kSh) == (lo >> kSh) && tk_index<DT>(j) <= last)) {
         const int i = atomicAdd(&count, 1);
-        if (i < a.cap) out[i] = ((uint64_t)k << 32) | (uint32_t)~(base + tk_index<DT>(j));
+        if (i < a.cap) out[i] = tk_pack(tk_value(k), ~(uint32_t)(base + tk_index<DT>(j)));   // (v[j] is gone)
       }
     }
     __syncthreads();
@@ -185,13 +193,14 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) at += w < wave ? red[w] : 0;
   out += __builtin_amdgcn_readfirstlane(at);
-  asm volatile("" : "+v"(thr));   // (the comparisons are made again, not kept in scalar registers)
+  uint32_t not0 = ~(uint32_t)(base + tk_index<DT>(0));   // and ~(i + d) is ~i - d
+  asm volatile("" : "+v"(thr), "+v"(not0));   // (the comparisons are made again, not kept in scalar registers)
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const uint64_t b = __ballot(v[j] >= thr);
     if (b) {   // uniform
       const uint32_t i = __builtin_amdgcn_mbcnt_hi((uint32_t)(b >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)b, 0));
-      if (v[j] >= thr) out[i] = ((uint64_t)tk_key(v[j]) << 32) | (uint32_t)~(base + tk_index<DT>(j));
+      if (v[j] >= thr) out[i] = tk_pack(v[j], not0 - (uint32_t)(tk_index<DT>(j) - tk_index<DT>(0)));
       out += __popcll(b);
     }
   }
@@ -201,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void k_tk_seg(TopkArgs a) {
 constexpr int kMergeCap = 1024;   // candidates that are ranked against each other
 constexpr int kRankStep = 16;
 
-// f(key) for each of this thread's candidates (0 for none), eight loads at a time.  The segments'
+// f(its key) for each of this thread's candidates (0 for none), eight loads at a time.  The segments'
 // lists are dealt out as one, candidate i to thread i mod 256: off[] holds where each list begins
 // in it, off[n_seg] their total.
 template <typename F>
@@ -224,12 +233,12 @@ __device__ __forceinline__ void each_candidate(const TopkArgs& a, const uint64_t
 #pragma unroll
     for (int q = 0; q < 8; ++q) k[q] = cand[(int64_t)seg[q] * a.cap + at[q] - off[seg[q]]];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f(i0 + q * kThreads < total ? k[q] : 0);
+    for (int q = 0; q < 8; ++q) f(i0 + q * kThreads < total ? tk_key_of(k[q]) : 0);
   }
 }
 
-// A few thousand candidates a row, so that latencies are what it takes: 7 us for one row, 12 us for
-// 512 (top 64), 14.5 us for 1027 (top 128).
+// A few thousand candidates a row, so that latencies are what it takes: 7 us for one row, 12.5 us
+// for 512 (top 64), 15 us for 1027 (top 128).
 template <int NM>
 __global__ __launch_bounds__(kThreads) void k_tk_merge(TopkArgs a) {
   __shared__ alignas(16) uint64_t key[kMergeCap + kRankStep];

@@ -79,7 +79,7 @@ struct TopkArgs {
   int32_t* index;                 // [R, K]
   float* logit;                   // [R, K]
   float* log_z;                   // [R] or nullptr
-  uint64_t* cand;                 // [R][n_seg][cap]: order key and complemented index
+  uint64_t* cand;                 // [R][n_seg][cap]: logit and complemented index
   int32_t* n_cand;                // [R][n_seg]
   MaxSum* ms;                     // [R][n_seg][4 waves]
 };
