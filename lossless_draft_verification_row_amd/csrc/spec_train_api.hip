@@ -36,8 +36,8 @@ bool dtype_valid(const spec_dtype& dt) {
   return v == SPEC_BF16 || v == SPEC_F32;
 }
 bool rows16(const void* p, int64_t ld, int elem) { return ((uintptr_t)p % 16) == 0 && (ld * elem) % 16 == 0; }
-bool temperature_valid(float t) { return t > 0.f && isfinite(t) && isfinite(1.f / t); }
 float exp2_scale(float t) { return (float)(1.4426950408889634 / (double)t); }
+bool temperature_valid(float t) { return t > 0.f && isfinite(t) && isfinite(exp2_scale(t)); }
 
 HlPlan hl_plan(int R, int V, int D) {
   HlPlan p;

@@ -61,3 +61,11 @@ def test_unknown_types_are_refused():
     for dt in (-1, 2, 7):
         assert lib.spec_row_topk(2, 10, 2, dt, 256, 10, 1.0, 256, 256, None, 256, 1 << 20, None) == -1
         assert lib.spec_topk_distill(2, 10, 2, dt, 256, 10, 256, 256, None, 1.0, None, 256, None, None, 0, 256, 1 << 20, None) == -1
+
+
+def test_temperatures_without_a_finite_scale_are_refused():
+    lib = L.load_library()
+    for T in (3e-39, 4.2e-39, 1e-45, 0.0, -1.0, float("inf"), float("nan")):
+        assert lib.spec_row_topk(2, 10, 2, 0, 256, 10, T, 256, 256, None, 256, 1 << 20, None) == -1, T
+        assert lib.spec_topk_distill(2, 10, 2, 0, 256, 10, 256, 256, None, T, None, 256, None, None, 0, 256, 1 << 20, None) == -1, T
+        assert lib.spec_lm_head_loss(2, 10, 64, 256, 64, 256, 64, 256, T, None, 256, None, None, 0, None, 0, 256, 1 << 30, None) == -1, T
